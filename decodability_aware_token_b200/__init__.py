@@ -15,7 +15,8 @@ import torch
 
 from . import _abi
 
-__all__ = ["FocusContext", "StepParams", "StepOutputs", "FocusError", "status_string", "library_path"]
+__all__ = ["FocusContext", "StepParams", "StepOutputs", "FocusError", "status_string", "library_path",
+           "ChunkContext", "ChunkPlan"]
 
 library_path = _abi.LIB_PATH
 
@@ -267,3 +268,6 @@ class FocusContext:
             self.close()
         except Exception:
             pass
+
+
+from .chunk import ChunkContext, ChunkPlan  # noqa: E402  (uses the checks above)

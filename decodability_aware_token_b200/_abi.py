@@ -18,6 +18,7 @@ FOCUS_DEVERR_PAGE_ID = 0x2
 FOCUS_DEVERR_PREFIX = 0x4
 FOCUS_DEVERR_TIMEOUT = 0x8
 FOCUS_DEVERR_FORCED_SET = 0x10
+FOCUS_DEVERR_ROWS = 0x20
 
 FOCUS_DTYPE_F32 = 0
 FOCUS_DTYPE_BF16 = 1
@@ -25,7 +26,9 @@ FOCUS_DTYPE_BF16 = 1
 # every symbol include/focus.h declares (checked by the CPU tests)
 EXPORTED = ("focus_init", "focus_step", "focus_destroy", "focus_status_string", "focus_get_device_error",
             "focus_workspace_bytes", "focus_last_step_launches", "focus_profile_begin", "focus_profile_end",
-            "focus_lm_head_conf_noalloc", "focus_commit_block", "focus_decode_block", "focus_probe_wait_timeout")
+            "focus_lm_head_conf_noalloc", "focus_commit_block", "focus_decode_block", "focus_probe_wait_timeout",
+            "focus_chunk_init", "focus_chunk_destroy", "focus_chunk_workspace_bytes", "focus_chunk_get_device_error",
+            "focus_chunk_plan_rows", "focus_chunk_qk_norm_rope", "focus_chunk_attention")
 
 KERNEL_CLASSES = ("embed_norm", "qkv_finalize", "attn_score", "attn_ragged", "row_norm", "select", "decode",
                   "gemm_full_qkv", "gemm_full_o", "gemm_full_gateup", "gemm_full_down",
@@ -68,6 +71,38 @@ class StepOut(C.Structure):
                 ("importance", C.c_void_p), ("hidden", C.c_void_p)]
 
 
+class ChunkCfg(C.Structure):
+    _fields_ = [("n_layers", C.c_int32), ("n_q_heads", C.c_int32), ("n_kv_heads", C.c_int32), ("head_dim", C.c_int32),
+                ("dtype", C.c_int32), ("rope_theta", C.c_float)]
+
+
+class ChunkLimits(C.Structure):
+    _fields_ = [("max_requests", C.c_int32), ("max_pages_per_req", C.c_int32)]
+
+
+class ChunkPlanArgs(C.Structure):
+    _fields_ = [("n_requests", C.c_int32), ("max_rows", C.c_int32), ("page_size", C.c_int32), ("n_pages", C.c_int32),
+                ("n_free", C.c_int32), ("prefix_len", C.c_void_p), ("new_len", C.c_void_p), ("page_table", C.c_void_p),
+                ("free_pages", C.c_void_p), ("free_head", C.c_void_p), ("row_offsets", C.c_void_p),
+                ("kv_len", C.c_void_p), ("row_req", C.c_void_p), ("row_pos", C.c_void_p), ("row_slot", C.c_void_p),
+                ("free_next", C.c_void_p)]
+
+
+class ChunkQkArgs(C.Structure):
+    _fields_ = [("rows", C.c_int32), ("layer", C.c_int32), ("page_size", C.c_int32), ("n_pages", C.c_int32),
+                ("eps", C.c_float), ("q_stride", C.c_int64), ("k_stride", C.c_int64), ("v_stride", C.c_int64),
+                ("out_stride", C.c_int64), ("q", C.c_void_p), ("k", C.c_void_p), ("v", C.c_void_p),
+                ("q_norm", C.c_void_p), ("k_norm", C.c_void_p), ("row_pos", C.c_void_p), ("row_slot", C.c_void_p),
+                ("q_out", C.c_void_p), ("kv_pool", C.c_void_p)]
+
+
+class ChunkAttnArgs(C.Structure):
+    _fields_ = [("n_requests", C.c_int32), ("rows", C.c_int32), ("max_new", C.c_int32), ("page_size", C.c_int32),
+                ("n_pages", C.c_int32), ("layer", C.c_int32), ("mask_block", C.c_int32), ("scale", C.c_float),
+                ("q_stride", C.c_int64), ("out_stride", C.c_int64), ("q", C.c_void_p), ("kv_pool", C.c_void_p),
+                ("row_offsets", C.c_void_p), ("kv_len", C.c_void_p), ("page_table", C.c_void_p), ("out", C.c_void_p)]
+
+
 _lib = None
 
 
@@ -107,5 +142,19 @@ def load():
     lib.focus_decode_block.argtypes = [C.c_void_p, C.POINTER(Batch), C.POINTER(Params), C.c_int32, C.POINTER(StepOut),
                                        C.POINTER(C.c_int32), C.c_void_p]
     lib.focus_decode_block.restype = C.c_int
+    lib.focus_chunk_init.argtypes = [C.POINTER(ChunkCfg), C.POINTER(ChunkLimits), C.POINTER(C.c_void_p)]
+    lib.focus_chunk_init.restype = C.c_int
+    lib.focus_chunk_destroy.argtypes = [C.c_void_p]
+    lib.focus_chunk_destroy.restype = C.c_int
+    lib.focus_chunk_workspace_bytes.argtypes = [C.POINTER(ChunkCfg), C.POINTER(ChunkLimits)]
+    lib.focus_chunk_workspace_bytes.restype = C.c_size_t
+    lib.focus_chunk_get_device_error.argtypes = [C.c_void_p, C.POINTER(C.c_int32)]
+    lib.focus_chunk_get_device_error.restype = C.c_int
+    lib.focus_chunk_plan_rows.argtypes = [C.c_void_p, C.POINTER(ChunkPlanArgs), C.c_void_p]
+    lib.focus_chunk_plan_rows.restype = C.c_int
+    lib.focus_chunk_qk_norm_rope.argtypes = [C.c_void_p, C.POINTER(ChunkQkArgs), C.c_void_p]
+    lib.focus_chunk_qk_norm_rope.restype = C.c_int
+    lib.focus_chunk_attention.argtypes = [C.c_void_p, C.POINTER(ChunkAttnArgs), C.c_void_p]
+    lib.focus_chunk_attention.restype = C.c_int
     _lib = lib
     return lib

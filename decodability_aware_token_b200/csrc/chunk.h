@@ -1,0 +1,50 @@
+// Internal interface of the prompt-chunk operators: the API file (chunk_api.cu) checks the arguments and
+// picks the kernels; each operator's kernels are in their own translation unit.
+#pragma once
+#include "launch.h"
+
+namespace focus {
+
+constexpr int kChunkCtas = 148;          // CTAs (one per SM of a B200) that share a split attention launch
+constexpr int kChunkMaxRequests = 16384; // the plan and the attention schedule keep per-request sums in shared memory
+
+struct ChunkPlanDev {
+    focus_chunk_plan p;
+    int max_pages;
+    int* arrivals;   // [1] zero between launches
+    int* err;
+};
+int launch_chunk_plan(const ChunkPlanDev& a, cudaStream_t s);
+bool configure_chunk_plan_kernel();
+
+struct ChunkQkDev {
+    focus_chunk_qk p;
+    int L, Hq, Hkv;
+    const double* freq_over_pi;  // [d / 2] theta^(-2i/d) / pi
+    int* err;
+};
+template <typename T, int D> int launch_chunk_qk(const ChunkQkDev& a, cudaStream_t s);
+
+struct ChunkAttnDev {
+    const void* q;
+    void* out;
+    const void* kv_pool;
+    const int32_t* row_offsets;
+    const int32_t* kv_len;
+    const int32_t* page_table;
+    long long q_stride, out_stride;  // elements
+    int N, rows, max_new, Hq, Hkv, G, L, layer, S, n_pages, max_pages, mask_block;
+    float scale;
+    // scratch of units whose key walk is split over CTAs: slot 2c / 2c + 1 is CTA c's first / last piece
+    float* part_o;
+    float* part_ml;
+    int* counters;   // [kChunkCtas] arrivals at the unit whose first piece is CTA c's; zero between launches
+    int* err;
+};
+// CUDA-core kernels: float32 models
+constexpr int kChunkSimtCtas = 2 * kChunkCtas;
+constexpr int kChunkSimtRows = 64;  // query vectors per unit
+template <typename T, int D> int launch_chunk_attention_simt(const ChunkAttnDev& a, int sms, cudaStream_t s);
+bool configure_chunk_attention_simt();
+
+}  // namespace focus

@@ -1,0 +1,240 @@
+// Work split of the chunk attention kernels.
+//
+// A unit is (request b, KV head g, tile k of `tok` tokens); it walks ceil(visible keys / KEYS) key blocks
+// (at least one, so that rows that see nothing are still written).  The units of a launch, in the order
+// b, g, k, form one line of W blocks, and CTA c of C takes blocks [W c / C, W (c + 1) / C): every CTA walks
+// the same number of key blocks whatever the lengths are, and at most its first and its last unit are
+// shared with neighbours.  Shared units write unnormalised partial results; the CTA that arrives last adds
+// them in block order, so the result does not depend on the order of arrival.
+//
+// Each CTA finds its own range from the lengths alone (a scan over the requests in shared memory, about a
+// microsecond): no scheduling kernel, no host copy of the lengths.
+#pragma once
+#include "chunk.h"
+
+namespace focus {
+namespace {
+
+struct ChunkReq {
+    int row0, n, kv;  // first row, rows, cached keys (n = 0: nothing to do)
+};
+
+// Request b's rows and keys; a request whose numbers are out of range is flagged and skipped.
+__device__ __forceinline__ ChunkReq chunk_req(const ChunkAttnDev& a, int b, bool flag) {
+    ChunkReq r;
+    r.row0 = a.row_offsets[b];
+    const int end = a.row_offsets[b + 1];
+    r.kv = a.kv_len[b];
+    r.n = 0;
+    if (r.row0 < 0 || end < r.row0 || end > a.rows || end - r.row0 > a.max_new) {
+        if (flag) raise_err(a.err, FOCUS_DEVERR_ROWS);
+    } else if (r.kv < 0 || r.kv > a.max_pages * a.S) {
+        if (flag) raise_err(a.err, FOCUS_DEVERR_PREFIX);
+    } else {
+        r.n = end - r.row0;
+    }
+    return r;
+}
+
+// Keys visible at position pos (the API clamps mask_block so that nothing overflows).
+__device__ __forceinline__ int chunk_visible(int pos, int kv, int mask_block) {
+    return pos < 0 ? 0 : min(kv, (pos / mask_block + 1) * mask_block);
+}
+
+// Key blocks of tile k
+template <int KEYS>
+__device__ __forceinline__ int chunk_tile_blocks(const ChunkReq& r, int mask_block, int tok, int k) {
+    const int last = min(r.n, (k + 1) * tok) - 1;
+    const int v = chunk_visible(r.kv - r.n + last, r.kv, mask_block);
+    return max(1, (v + KEYS - 1) / KEYS);
+}
+
+// Which requests a kernel serves: lo < n G <= hi.
+struct ChunkShape {
+    int tok, lo, hi;
+};
+__device__ __forceinline__ int chunk_tiles(const ChunkAttnDev& a, const ChunkShape& sh, const ChunkReq& r) {
+    const long long v = (long long)r.n * a.G;
+    return v > sh.lo && v <= sh.hi ? (r.n + sh.tok - 1) / sh.tok : 0;
+}
+
+struct ChunkRange {
+    long long W, w0, w1;  // all blocks, this CTA's range (w0 == w1: none)
+    int C;                // CTAs that share the line
+    int b, g, k, blk;     // where w0 lies
+};
+
+// CTA whose range holds block w: the largest c with floor(W c / C) <= w.
+__device__ __forceinline__ int chunk_owner(long long w, long long W, int C) {
+    return (int)(((w + 1) * C - 1) / W);
+}
+
+// Fill *out (shared memory) for this CTA.  `scr` holds N + 1 long longs of shared memory, `red` 32.  Every
+// thread of the block calls it; it ends with a barrier.  min_blocks: smallest useful share of a CTA.
+template <int KEYS>
+__device__ void chunk_schedule(const ChunkAttnDev& a, const ChunkShape& sh, int min_blocks, long long* scr,
+                               long long* red, ChunkRange* out) {
+    const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
+    // blocks of one KV head per request; requests of many tiles are left to whole warps
+    constexpr int kSerial = 4;
+    int any_long = 0;
+    for (int b = tid; b < a.N; b += nt) {
+        const ChunkReq r = chunk_req(a, b, blockIdx.x == 0);
+        const int tiles = chunk_tiles(a, sh, r);
+        long long s = 0;
+        if (tiles <= kSerial) {
+            for (int k = 0; k < tiles; ++k) s += chunk_tile_blocks<KEYS>(r, a.mask_block, sh.tok, k);
+        } else {
+            s = -1;
+            any_long = 1;
+        }
+        scr[b] = s;
+    }
+    if (__syncthreads_or(any_long)) {
+        for (int b = warp; b < a.N; b += nw) {
+            if (scr[b] >= 0) continue;
+            const ChunkReq r = chunk_req(a, b, false);
+            const int tiles = chunk_tiles(a, sh, r);
+            long long s = 0;
+            for (int k = lane; k < tiles; k += 32) s += chunk_tile_blocks<KEYS>(r, a.mask_block, sh.tok, k);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            if (lane == 0) scr[b] = s;
+            __syncwarp();
+        }
+        __syncthreads();
+    }
+    // inclusive scan over the requests (all KV heads)
+    long long carry = 0;
+    for (int b0 = 0; b0 < a.N; b0 += nt) {
+        const int b = b0 + tid;
+        long long v = b < a.N ? scr[b] * a.Hkv : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += u;
+        }
+        if (lane == 31) red[warp] = v;
+        __syncthreads();
+        long long before = carry, all = 0;
+        for (int w = 0; w < nw; ++w) {
+            if (w < warp) before += red[w];
+            all += red[w];
+        }
+        if (b < a.N) scr[b] = before + v;
+        carry += all;
+        __syncthreads();
+    }
+    const long long W = carry;
+    const long long want = (W + min_blocks - 1) / min_blocks;
+    const int C = (int)(want < gridDim.x ? want : (long long)gridDim.x);
+    const int c = blockIdx.x;
+    const long long w0 = C > 0 && c < C ? W * c / C : 0, w1 = C > 0 && c < C ? W * (c + 1) / C : 0;
+    if (tid == 0) {
+        out->W = W;
+        out->C = C;
+        out->w0 = w0;
+        out->w1 = w1;
+        out->b = out->g = out->k = out->blk = 0;
+    }
+    __syncthreads();
+    if (w0 < w1) {
+        for (int b = tid; b < a.N; b += nt)
+            if (scr[b] > w0 && (b == 0 || scr[b - 1] <= w0)) out->b = b;
+        __syncthreads();
+        if (warp == 0) {
+            const int b = out->b;
+            const long long base = b ? scr[b - 1] : 0;
+            const long long per = (scr[b] - base) / a.Hkv;  // blocks of one KV head
+            const int g = (int)((w0 - base) / per);
+            long long rem = w0 - base - (long long)g * per;
+            const ChunkReq r = chunk_req(a, b, false);
+            const int tiles = chunk_tiles(a, sh, r);
+            for (int k0 = 0; k0 < tiles; k0 += 32) {
+                const int k = k0 + lane;
+                const long long mine = k < tiles ? chunk_tile_blocks<KEYS>(r, a.mask_block, sh.tok, k) : 0;
+                long long v = mine;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long u = __shfl_up_sync(0xffffffffu, v, o);
+                    if (lane >= o) v += u;
+                }
+                const bool here = v > rem && v - mine <= rem;
+                if (here) {
+                    out->g = g;
+                    out->k = k;
+                    out->blk = (int)(rem - (v - mine));
+                }
+                if (__any_sync(0xffffffffu, here)) break;
+                rem -= __shfl_sync(0xffffffffu, v, 31);
+            }
+        }
+    }
+    __syncthreads();
+}
+
+// One thread's walk along its CTA's range, unit piece by unit piece.
+template <int KEYS>
+struct ChunkWalk {
+    long long w, w1;   // next block, end
+    int b, g, k;       // the unit at w
+    int blk0, blk1;    // the piece's blocks within the unit
+    int nblk;          // blocks of the whole unit
+    int tiles;
+    ChunkReq r;
+
+    __device__ __forceinline__ void start(const ChunkAttnDev& a, const ChunkShape& sh, const ChunkRange& rg) {
+        w = rg.w0;
+        w1 = rg.w1;
+        b = rg.b;
+        g = rg.g;
+        k = rg.k;
+        blk0 = rg.blk;
+        if (w < w1) {
+            r = chunk_req(a, b, false);
+            tiles = chunk_tiles(a, sh, r);
+            fit(a, sh);
+        }
+    }
+    __device__ __forceinline__ bool live() const { return w < w1; }
+    __device__ __forceinline__ void fit(const ChunkAttnDev& a, const ChunkShape& sh) {
+        nblk = chunk_tile_blocks<KEYS>(r, a.mask_block, sh.tok, k);
+        const long long left = w1 - w;
+        blk1 = nblk - blk0 <= left ? nblk : blk0 + (int)left;
+    }
+    __device__ __forceinline__ void next(const ChunkAttnDev& a, const ChunkShape& sh) {
+        w += blk1 - blk0;
+        if (w >= w1) return;
+        blk0 = 0;
+        if (++k == tiles) {
+            k = 0;
+            if (++g == a.Hkv) {
+                g = 0;
+                do {  // the range ends inside the line, so a request with work follows
+                    if (++b >= a.N) {
+                        w = w1;  // (only if the lengths changed under the launch)
+                        return;
+                    }
+                    r = chunk_req(a, b, false);
+                    tiles = chunk_tiles(a, sh, r);
+                } while (tiles == 0);
+            }
+        }
+        fit(a, sh);
+    }
+    __device__ __forceinline__ bool whole() const { return blk0 == 0 && blk1 == nblk; }
+    // the CTAs that hold the unit's pieces, and this CTA's slot for its piece
+    __device__ __forceinline__ void pieces(const ChunkRange& rg, int& c0, int& c1) const {
+        const long long u0 = w - blk0;
+        c0 = chunk_owner(u0, rg.W, rg.C);
+        c1 = chunk_owner(u0 + nblk - 1, rg.W, rg.C);
+    }
+    // slot of CTA c's piece of this unit: its first piece unless the unit starts inside its range
+    __device__ __forceinline__ int slot(const ChunkRange& rg, int c) const {
+        const long long u0 = w - blk0;
+        return 2 * c + (rg.W * c / rg.C < u0 ? 1 : 0);
+    }
+};
+
+}  // namespace
+}  // namespace focus

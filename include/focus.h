@@ -80,6 +80,7 @@ extern "C" {
 #define FOCUS_DEVERR_PREFIX      0x4   /* prefix_len < 0 or beyond the page table -- clamped */
 #define FOCUS_DEVERR_TIMEOUT     0x8   /* a pipeline wait gave up -- outputs are invalid */
 #define FOCUS_DEVERR_FORCED_SET  0x10  /* forced keep set not ascending / out of range -- request keeps nothing */
+#define FOCUS_DEVERR_ROWS        0x20  /* chunk row range or new-token count out of range -- request skipped */
 
 typedef enum { FOCUS_DTYPE_F32 = 0, FOCUS_DTYPE_BF16 = 1 } focus_dtype;
 
@@ -303,6 +304,154 @@ int focus_profile_end(focus_ctx* ctx, float* total_ms, int32_t* launches);
 int focus_lm_head_conf_noalloc(const float* hidden, int32_t rows, int32_t hidden_dim, const void* final_norm,
                                const void* lm_head, int32_t vocab, float rms_eps, float* conf, int32_t* top_id,
                                void* stream);
+
+/* ---- prompt chunks over the paged cache -----------------------------------------
+ * The focused step reads prefix pages that already hold the prompt's keys and values.  These calls fill
+ * them: a chunk of new tokens per request (a whole prompt, a slice of one, or a single token) is given
+ * pages and rows, its keys and values are written into the pages, and its queries attend over everything
+ * the request has cached.  Usual order, per chunk: focus_chunk_plan_rows once, then per layer
+ * focus_chunk_qk_norm_rope and focus_chunk_attention.
+ *
+ * A focus_chunk_ctx holds what the calls need beside their arguments: scratch for attention that is split
+ * over the key axis, the rotary frequencies, and a device error word of its own.  Its size does not depend
+ * on the number of tokens.  Every call is asynchronous on `stream`, allocates nothing and can be captured
+ * in a CUDA graph.  As with focus_step, two calls (or two replayed graphs) of one context must not overlap
+ * in time; use one context per stream that runs concurrently.  The device current at a call must be the
+ * context's.  Rows of a chunk are numbered 0 .. rows - 1: request b owns row_offsets[b] ..
+ * row_offsets[b + 1] - 1, and rows from row_offsets[N] on belong to nobody. */
+typedef struct {
+    int32_t n_layers;    /* L of the KV pool (>= 1) */
+    int32_t n_q_heads;   /* Hq, a multiple of n_kv_heads; Hq / Hkv <= 64 */
+    int32_t n_kv_heads;  /* Hkv */
+    int32_t head_dim;    /* d: 64 or 128 (bf16 needs 128) */
+    int32_t dtype;       /* focus_dtype */
+    float   rope_theta;  /* RoPE base: pair i turns by pos * theta^(-2i/d) */
+} focus_chunk_cfg;
+
+typedef struct {
+    int32_t max_requests;       /* N bound, <= 16384 */
+    int32_t max_pages_per_req;  /* row length of page_table */
+} focus_chunk_limits;
+
+typedef struct focus_chunk_ctx focus_chunk_ctx;
+
+/* Validate and allocate.  Returns FOCUS_OK and *out, or an error with *out = NULL: FOCUS_ERR_INVALID_ARG
+ * (null pointer, inconsistent heads, bad dtype, theta <= 0, a limit <= 0), FOCUS_ERR_UNSUPPORTED (head_dim,
+ * more than 64 query heads per KV head), FOCUS_ERR_LIMITS (max_requests > 16384), FOCUS_ERR_NO_MEMORY or
+ * FOCUS_ERR_CUDA. */
+int focus_chunk_init(const focus_chunk_cfg* cfg, const focus_chunk_limits* lim, focus_chunk_ctx** out);
+
+/* Free the workspace.  Synchronises the device first.  NULL is accepted. */
+int focus_chunk_destroy(focus_chunk_ctx* ctx);
+
+/* Size in bytes of the workspace such a context allocates (0 on bad arguments). */
+size_t focus_chunk_workspace_bytes(const focus_chunk_cfg* cfg, const focus_chunk_limits* lim);
+
+/* As focus_get_device_error, for the chunk context's own error word. */
+int focus_chunk_get_device_error(focus_chunk_ctx* ctx, int32_t* bits);
+
+/* Pages, rows and cache slots of a chunk, from the request lengths alone (one launch, no host sync).
+ * With S = page_size, have_b = ceil(prefix_len[b] / S) pages already in the table and need_b =
+ * ceil((prefix_len[b] + new_len[b]) / S) - have_b:
+ *   - request b is PLACED iff the rows asked for by requests 0 .. b fit in max_rows (always, when it asks
+ *     for none) and, if it needs pages, the pages needed by requests 0 .. b that passed the row test fit in
+ *     the free list behind *free_head.  Nobody overtakes a request that needs pages.
+ *   - a placed request gets pages free_pages[*free_head + (pages taken by earlier requests) ...], written to
+ *     page_table[b][have_b ...], and new_len[b] rows; any other request gets no rows and no pages.
+ *   - row r of request b at index i: row_req = b, row_pos = prefix_len[b] + i, row_slot = page * S +
+ *     row_pos % S (-1 if the table holds no valid page for it).  Rows past the last get -1 in all three.
+ *   - row_offsets [N + 1], kv_len[b] = prefix_len[b] + (rows of b), *free_next = *free_head + pages taken.
+ * A request with a negative length or with prefix_len + new_len beyond the page table sets
+ * FOCUS_DEVERR_PREFIX and is not placed; *free_head outside [0, n_free] sets FOCUS_DEVERR_PAGE_ID and
+ * counts as an empty list; a free list entry outside [0, n_pages) sets FOCUS_DEVERR_PAGE_ID when it is
+ * taken, and so does a table entry outside that range that a new row falls on.  Entries of the free list
+ * must differ from each other and from the pages in use.  free_next may be free_head; the other outputs
+ * must not overlap the inputs. */
+typedef struct {
+    int32_t n_requests;           /* N */
+    int32_t max_rows;             /* rows the row_* outputs hold */
+    int32_t page_size;            /* S */
+    int32_t n_pages;              /* pages in the pool (n_pages * S < 2^31) */
+    int32_t n_free;               /* entries of free_pages */
+    const int32_t* prefix_len;    /* [N] cached tokens */
+    const int32_t* new_len;       /* [N] new tokens, 0 allowed */
+    int32_t* page_table;          /* [N, max_pages_per_req] in place */
+    const int32_t* free_pages;    /* [n_free] */
+    const int32_t* free_head;     /* [1] first free entry */
+    int32_t* row_offsets;         /* [N + 1] out */
+    int32_t* kv_len;              /* [N] out */
+    int32_t* row_req;             /* [max_rows] out */
+    int32_t* row_pos;             /* [max_rows] out */
+    int32_t* row_slot;            /* [max_rows] out */
+    int32_t* free_next;           /* [1] out */
+} focus_chunk_plan;
+/* Returns FOCUS_OK, FOCUS_ERR_INVALID_ARG, FOCUS_ERR_LIMITS (N, or n_pages * S >= 2^31) or FOCUS_ERR_CUDA. */
+int focus_chunk_plan_rows(focus_chunk_ctx* ctx, const focus_chunk_plan* p, void* stream);
+
+/* Queries and keys of a chunk: per-head RMSNorm x / sqrt(mean(x^2) + eps) * gain (either gain may be NULL:
+ * that side is not normed), rotate-half RoPE at row_pos, both in float32 with one rounding to T at the end;
+ * queries go to q_out, keys and (unchanged) values into the pool at row_slot, layer `layer`.
+ * A row with row_pos < 0 is skipped (its q_out row stays as it was); a row with row_slot < 0 gets its
+ * queries but is not stored; row_slot >= n_pages * S sets FOCUS_DEVERR_PAGE_ID and is not stored.  Slots of
+ * stored rows must differ.  q_out may be q (same stride). */
+typedef struct {
+    int32_t rows;
+    int32_t layer;
+    int32_t page_size;            /* S */
+    int32_t n_pages;
+    float   eps;
+    int64_t q_stride;             /* elements between consecutive rows of q (>= Hq d) ... */
+    int64_t k_stride;             /* ... of k and of v (>= Hkv d) */
+    int64_t v_stride;
+    int64_t out_stride;           /* ... of q_out (>= Hq d) */
+    const void* q;                /* [rows, Hq, d] T; heads dense within a row.  q, k, v, q_out and kv_pool */
+    const void* k;                /* [rows, Hkv, d]   are 16-byte aligned, and so are their rows */
+    const void* v;                /* [rows, Hkv, d] */
+    const void* q_norm;           /* [d] T, 16-byte aligned, or NULL */
+    const void* k_norm;           /* [d] T, 16-byte aligned, or NULL */
+    const int32_t* row_pos;       /* [rows] */
+    const int32_t* row_slot;      /* [rows] */
+    void* q_out;                  /* [rows, Hq, d] out */
+    void* kv_pool;                /* [n_pages, L, 2, Hkv, S, d] T, in place */
+} focus_chunk_qk;
+/* Returns FOCUS_OK, FOCUS_ERR_INVALID_ARG, FOCUS_ERR_LIMITS (n_pages * S >= 2^31) or FOCUS_ERR_CUDA. */
+int focus_chunk_qk_norm_rope(focus_chunk_ctx* ctx, const focus_chunk_qk* p, void* stream);
+
+/* Attention of a chunk over the paged cache.  Request b has n_b = row_offsets[b + 1] - row_offsets[b] rows,
+ * the last n_b of its kv_len[b] positions; row i sits at position p = kv_len[b] - n_b + i and sees the keys
+ * j < min(kv_len[b], (p / M + 1) M) with M = mask_block: M = 1 is the causal mask, M = B lets a block of B
+ * positions see each other (block-diffusion prompts), M >= kv_len[b] is full attention.
+ *   out[row, h] = sum_j softmax_j(scale q[row, h] . K[j]) V[j],   KV head h / (Hq / Hkv),
+ * with float32 scores, maxima, sums and accumulators; bf16 weights are rounded once before the product
+ * with V.  A row that sees no key (kv_len[b] < n_b) gets zeros; rows of no request stay as they were.
+ * Cache entries no row of a request sees, and pages' tails past kv_len, may hold anything, NaN included;
+ * V of a key that some row of the request sees has to be finite.
+ * A row range outside [0, rows], decreasing, or longer than max_new sets FOCUS_DEVERR_ROWS and skips the
+ * request; kv_len outside [0, max_pages_per_req * S] sets FOCUS_DEVERR_PREFIX and skips it; a page id
+ * outside [0, n_pages) sets FOCUS_DEVERR_PAGE_ID and its keys are not attended to.  Row ranges of different
+ * requests must not overlap.  Results do not depend on other requests' values; the split of a long key walk
+ * does depend on the batch's lengths, so the order of float32 sums may. */
+typedef struct {
+    int32_t n_requests;           /* N */
+    int32_t rows;                 /* rows q and out hold */
+    int32_t max_new;              /* bound on n_b (>= 1); a tight one saves a launch */
+    int32_t page_size;            /* S: bf16 16, 32 or 64; float32 any */
+    int32_t n_pages;
+    int32_t layer;
+    int32_t mask_block;           /* M >= 1 */
+    float   scale;                /* > 0; 0 stands for 1 / sqrt(d) */
+    int64_t q_stride;             /* elements between consecutive rows of q and of out (>= Hq d) */
+    int64_t out_stride;
+    const void* q;                /* [rows, Hq, d] T; q, out and kv_pool and their rows 16-byte aligned */
+    const void* kv_pool;          /* [n_pages, L, 2, Hkv, S, d] T */
+    const int32_t* row_offsets;   /* [N + 1] */
+    const int32_t* kv_len;        /* [N] */
+    const int32_t* page_table;    /* [N, max_pages_per_req] */
+    void* out;                    /* [rows, Hq, d] T; must not overlap q */
+} focus_chunk_attn;
+/* Returns FOCUS_OK, FOCUS_ERR_INVALID_ARG, FOCUS_ERR_LIMITS (N, or max_pages_per_req * S > 2^30),
+ * FOCUS_ERR_UNSUPPORTED (bf16 page size) or FOCUS_ERR_CUDA. */
+int focus_chunk_attention(focus_chunk_ctx* ctx, const focus_chunk_attn* p, void* stream);
 
 #ifdef __cplusplus
 }
