@@ -41,6 +41,12 @@ struct ChunkAttnDev {
     int* counters;   // [kChunkCtas] arrivals at the unit whose first piece is CTA c's; zero between launches
     int* err;
 };
+// bf16 models: requests of at most kChunkFewRows query vectors per KV head (single tokens) and the others
+constexpr int kChunkFewRows = 8;
+constexpr int kChunkTileRows = 256;  // query vectors per unit of the tile kernel
+int launch_chunk_attention_tile(const ChunkAttnDev& a, int sms, cudaStream_t s);
+bool configure_chunk_attention_tile();
+
 // CUDA-core kernels: float32 models
 constexpr int kChunkSimtCtas = 2 * kChunkCtas;
 constexpr int kChunkSimtRows = 64;  // query vectors per unit

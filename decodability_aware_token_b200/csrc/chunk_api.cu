@@ -42,7 +42,8 @@ size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 // words: error word, plan arrivals, attention counters (all zero between calls)
 Layout plan_layout(const focus_chunk_cfg* c) {
-    const size_t vecs = (size_t)2 * kChunkSimtCtas * kChunkSimtRows;
+    const size_t vecs = c->dtype == FOCUS_DTYPE_BF16 ? (size_t)2 * kChunkCtas * kChunkTileRows
+                                                     : (size_t)2 * kChunkSimtCtas * kChunkSimtRows;
     Layout l{};
     l.freq = 0;
     l.words = align_up(l.freq + (size_t)c->head_dim / 2 * 8, 256);
@@ -115,7 +116,7 @@ int focus_chunk_init(const focus_chunk_cfg* cfg, const focus_chunk_limits* lim, 
         freq[i] = pow((double)cfg->rope_theta, -2.0 * i / cfg->head_dim) / 3.14159265358979323846;
     if (cudaMemcpy(c->freq_over_pi, freq, (size_t)cfg->head_dim / 2 * 8, cudaMemcpyHostToDevice) != cudaSuccess ||
         cudaMemset(c->err, 0, l.part_ml - l.words) != cudaSuccess || !configure_chunk_plan_kernel() ||
-        !configure_chunk_attention_simt() || cudaDeviceSynchronize() != cudaSuccess) {
+        !configure_chunk_attention_simt() || !configure_chunk_attention_tile() || cudaDeviceSynchronize() != cudaSuccess) {
         (void)cudaGetLastError();
         cudaFree(c->ws);
         delete c;
@@ -205,7 +206,11 @@ int focus_chunk_attention(focus_chunk_ctx* c, const focus_chunk_attn* p, void* s
         p->layer >= c->cfg.n_layers || p->mask_block < 1 || !(p->scale >= 0.f) || !isfinite(p->scale))
         return FOCUS_ERR_INVALID_ARG;
     const int64_t max_kv = (int64_t)c->lim.max_pages_per_req * p->page_size;
-    if (p->n_requests > c->lim.max_requests || max_kv > ((int64_t)1 << 30)) return FOCUS_ERR_LIMITS;
+    // rows of the pool are addressed by 32-bit TMA coordinates
+    const int64_t pool_rows = (int64_t)p->n_pages * c->cfg.n_layers * 2 * c->cfg.n_kv_heads;
+    if (p->n_requests > c->lim.max_requests || max_kv > ((int64_t)1 << 30) ||
+        pool_rows >= ((int64_t)1 << 31) / p->page_size)
+        return FOCUS_ERR_LIMITS;
     const bool bf = c->cfg.dtype == FOCUS_DTYPE_BF16;
     if (bf && p->page_size != 16 && p->page_size != 32 && p->page_size != 64) return FOCUS_ERR_UNSUPPORTED;
     if (p->n_requests == 0 || p->rows == 0) return FOCUS_OK;
@@ -244,9 +249,14 @@ int focus_chunk_attention(focus_chunk_ctx* c, const focus_chunk_attn* p, void* s
     a.err = c->err;
     Range range("chunk_attention");
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int n = bf                        ? launch_chunk_attention_simt<bf16, 128>(a, c->sms, s)
-                  : c->cfg.head_dim == 64   ? launch_chunk_attention_simt<float, 64>(a, c->sms, s)
-                                            : launch_chunk_attention_simt<float, 128>(a, c->sms, s);
+    int n;
+    if (bf) {
+        n = launch_chunk_attention_simt<bf16, 128>(a, c->sms, s);
+        if (n >= 0 && (int64_t)a.max_new * a.G > kChunkFewRows) n = launch_chunk_attention_tile(a, c->sms, s);
+    } else {
+        n = c->cfg.head_dim == 64 ? launch_chunk_attention_simt<float, 64>(a, c->sms, s)
+                                  : launch_chunk_attention_simt<float, 128>(a, c->sms, s);
+    }
     return n < 0 ? FOCUS_ERR_CUDA : FOCUS_OK;
 }
 

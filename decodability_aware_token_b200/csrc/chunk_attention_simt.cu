@@ -352,7 +352,7 @@ template <typename T, int D> int launch_chunk_attention_simt(const ChunkAttnDev&
     const dim3 grid(2 * sms < kChunkSimtCtas ? 2 * sms : kChunkSimtCtas), block(kThreads);
     int n = 0;
     const long long most = (long long)a.max_new * a.G;
-    if (most > kFew) {  // units of 64 query vectors
+    if (most > kFew && sizeof(T) == 4) {  // units of 64 query vectors
         if (launched(launch_pdl(chunk_attn_simt_kernel<T, D, 64>, grid, block, simt_smem<D, 64>(a.N), s, 0, a)) < 0)
             return -1;
         ++n;

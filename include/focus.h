@@ -449,8 +449,8 @@ typedef struct {
     const int32_t* page_table;    /* [N, max_pages_per_req] */
     void* out;                    /* [rows, Hq, d] T; must not overlap q */
 } focus_chunk_attn;
-/* Returns FOCUS_OK, FOCUS_ERR_INVALID_ARG, FOCUS_ERR_LIMITS (N, or max_pages_per_req * S > 2^30),
- * FOCUS_ERR_UNSUPPORTED (bf16 page size) or FOCUS_ERR_CUDA. */
+/* Returns FOCUS_OK, FOCUS_ERR_INVALID_ARG, FOCUS_ERR_LIMITS (N, max_pages_per_req * S > 2^30, or a pool of
+ * 2^31 key and value rows or more), FOCUS_ERR_UNSUPPORTED (bf16 page size) or FOCUS_ERR_CUDA. */
 int focus_chunk_attention(focus_chunk_ctx* ctx, const focus_chunk_attn* p, void* stream);
 
 #ifdef __cplusplus
