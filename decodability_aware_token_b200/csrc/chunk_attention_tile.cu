@@ -32,9 +32,6 @@ using tc::idesc_bf16;
 using tc::mbar_arrive;
 using tc::mbar_expect_tx;
 using tc::mbar_init;
-using tc::mbar_wait;
-using tc::mma_bf16;
-using tc::mma_commit;
 using tc::smem_desc_sw128;
 using tc::smem_u32;
 using tc::tc_fence_after;
@@ -46,14 +43,20 @@ constexpr int kD = 128;
 constexpr int kKeys = 128;                    // keys per block
 constexpr int kHalf = 128 * 128;              // [128 rows][64 columns] bf16: 16 KB
 constexpr int kSlot = 2 * kHalf;              // K or V of one block: 32 KB
-constexpr int kSlots = 5;
+constexpr int kSlots = 4;
 constexpr int kQTile = 2 * kHalf;             // one query tile: 32 KB
 constexpr int kSmem = 2 * kQTile + kSlots * kSlot + 1024;
-constexpr int kTileThreads = 384;             // warps 0-3, 4-7: softmax of tile 0, 1; 8: copies; 9: MMAs
+constexpr int kSoftWarps = 8;                 // 4 per tile: one thread per query vector
+constexpr int kFirst = 96;                    // keys of a block whose weights are handed over first
+constexpr int kTileThreads = 32 * kSoftWarps + 128;  // then one warp for the copies and one for the MMAs
+constexpr int kCopyWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
 constexpr int kFlags = 8;                     // bad-page flags, one per block in flight
+constexpr int kUnits = 4;                     // unit descriptors in flight
 constexpr float kRaise = 8.f;
-static_assert(kSmem <= 227 * 1024, "shared memory");
-static_assert((kChunkMaxRequests + 1) * 8 <= kSlots * kSlot, "the schedule's sums fit in the ring");
+constexpr float kExp1 = 0.69328290f, kExp2 = 0.24221095f, kExp3 = 0.05500893f;
+constexpr int kPolyOf8 = 2;                   // of 8 pairs of weights, those computed on the FMA pipe
+static_assert(kSmem <= 220 * 1024, "shared memory");
+static_assert(kChunkMaxRequests * 8 <= kSlots * kSlot, "the schedule's sums fit in the ring");
 
 __device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* bar, void* dst, int x, int y, int z) {
     asm volatile(
@@ -62,13 +65,37 @@ __device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* ba
         : "memory");
 }
 
-// A (the weights) in TMEM, B in shared memory
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+// The MMA warp runs its loop with all lanes and one elected lane issues: loop counters and descriptors stay
+// uniform, which the issue needs (a loop inside `if (lane == 0)` issued one MMA per 85 cycles, slower than
+// the 64 that one takes).
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}\n" : "=r"(e));
+    return e;
+}
+__device__ __forceinline__ void mma_ss(uint32_t elected, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
-        ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc));
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n"
+        ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(elected));
+}
+// A (the weights) in TMEM, B in shared memory
+__device__ __forceinline__ void mma_ts(uint32_t elected, uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                       uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc), "r"(elected));
+}
+__device__ __forceinline__ void commit_one(uint32_t elected, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n"
+        ::"r"(smem_u32(bar)), "r"(elected)
+        : "memory");
 }
 
 // V tile as MN-major operand: 64 columns per 128-byte row, keys on consecutive rows, the next 64 columns
@@ -120,6 +147,14 @@ __device__ __forceinline__ void tm_st(uint32_t taddr, const uint32_t* r) {
           "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
+__device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -127,20 +162,104 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// two float32 in one 64-bit register: the FMA pipe takes both in one instruction
+__device__ __forceinline__ uint64_t f2(uint32_t lo, uint32_t hi) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+    return d;
+}
+__device__ __forceinline__ uint64_t f2(float lo, float hi) { return f2(__float_as_uint(lo), __float_as_uint(hi)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+    return d;
+}
+__device__ __forceinline__ uint64_t exp2_mufu(uint64_t x) {
+    return f2(ex2(__uint_as_float((uint32_t)x)), ex2(__uint_as_float((uint32_t)(x >> 32))));
+}
+// 2^x for x <= 8 on the FMA pipe: x = n + f with n the nearest integer (adding 1.5 2^23 leaves it in the low
+// mantissa bits), 2^f by a cubic with value 1 at 0 (least maximal relative error on [-1/2, 1/2], fitted by
+// reweighted least squares: 1.0e-4, a thirty-eighth of the half step the weight is rounded by), n added to
+// the exponent.  x is held at -127, where the result is exactly 0 (1.0's exponent bits cancel): a masked
+// score gets no weight.
+__device__ __forceinline__ float max_nan(float x, float y) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(x), "f"(y));
+    return d;
+}
+template <int N> __device__ __forceinline__ void exp2_poly_n(uint64_t* x) {
+    uint64_t n[N], f[N], p[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        x[i] = f2(max_nan(__uint_as_float((uint32_t)x[i]), -127.f), max_nan(__uint_as_float((uint32_t)(x[i] >> 32)), -127.f));
+#pragma unroll
+    for (int i = 0; i < N; ++i) n[i] = add2(x[i], f2(12582912.f, 12582912.f));
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = add2(n[i], f2(-12582912.f, -12582912.f));
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = fma2(f[i], f2(-1.f, -1.f), x[i]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = fma2(f2(kExp3, kExp3), f[i], f2(kExp2, kExp2));
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = fma2(p[i], f[i], f2(kExp1, kExp1));
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = fma2(p[i], f[i], f2(1.f, 1.f));
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        x[i] = f2((uint32_t)p[i] + ((uint32_t)n[i] << 23), (uint32_t)(p[i] >> 32) + ((uint32_t)(n[i] >> 32) << 23));
+}
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-__device__ __forceinline__ void sync_group(int t) {
-    if (t == 0) asm volatile("bar.sync 1, 128;" ::: "memory");
-    else asm volatile("bar.sync 2, 128;" ::: "memory");
+// The four warps of tile t meet (named barriers 1, 2).
+__device__ __forceinline__ void sync_tile(int t) { asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory"); }
+__device__ __forceinline__ bool tile_agrees(int t, bool ok) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "bar.red.and.pred p, %1, 128, q;\n\tselp.b32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(all)
+        : "r"(1 + t), "r"((uint32_t)ok)
+        : "memory");
+    return all != 0;
 }
 
-// Registers by role: 384 threads start with 168 each (64512); the two softmax warpgroups hold a row's 128
-// scores, the third (copies, MMAs) needs few: 2 x 128 x 208 + 128 x 88 = 64512.
+// As tc::mbar_wait, but the clock is read only every 64 failed tries: the waiting warps share their SM
+// quarter's issue slots with the ones that work.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, int* err) {
+    const uint32_t addr = smem_u32(bar);
+    if (tc::mbar_try(addr, parity)) return true;
+    const long long t0 = clock64();
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (tc::mbar_try(addr, parity)) return true;
+        if (clock64() - t0 > tc::kWaitCycles) {
+            raise_err(err, FOCUS_DEVERR_TIMEOUT);
+            return false;
+        }
+    }
+}
+
+// Registers by role: 384 threads start with 168 each (64512); the softmax warps hold a row's 128 scores, the
+// last warpgroup (copies, MMAs) needs few: 256 x 208 + 128 x 88 = 64512.
 constexpr int kSoftRegs = 208, kIssueRegs = 88;
-static_assert(2 * 128 * kSoftRegs + 128 * kIssueRegs <= 384 * 168, "register split");
+static_assert(32 * kSoftWarps * kSoftRegs + 128 * kIssueRegs <= kTileThreads * 168, "register split");
+
+// One piece of a unit, written by the copy thread as it reaches it and read by the other roles.
+struct UnitDesc {
+    int row0, n, kv;          // the request
+    int g, tok0;              // KV head, first token
+    int blk0, nb;             // key blocks of the piece (nb = 0: no more units)
+    int c0, c1, slot0;        // CTAs that hold pieces (c0 = -1: the whole unit is here), scratch slot of c0's
+};
 
 __global__ void __launch_bounds__(kTileThreads, 1)
 chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_constant__ CUtensorMap q_map,
@@ -149,8 +268,9 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* q_s = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* ring = q_s + 2 * kQTile;
-    __shared__ __align__(8) uint64_t q_full, q_empty, kv_full[kSlots], kv_empty[kSlots], s_full[2], p_full[2], o_full[2],
-        done_bar;
+    __shared__ __align__(8) uint64_t q_full, q_empty, kv_full[kSlots], kv_empty[kSlots], s_full[2], p_full[2][2],
+        o_full[2], done_bar, u_full[kUnits], u_empty[kUnits];
+    __shared__ UnitDesc unit_s[kUnits];
     __shared__ uint32_t bad_s[kFlags];  // per block: 16-key groups whose page id is invalid
     __shared__ uint32_t tmem_slot;
     __shared__ ChunkRange rg;
@@ -167,19 +287,24 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(&s_full[t], 1);
-            mbar_init(&p_full[t], 4);  // one arrival per softmax warp
+            mbar_init(&p_full[t][0], 4);  // one arrival per softmax warp
+            mbar_init(&p_full[t][1], 4);
             mbar_init(&o_full[t], 1);
+        }
+        for (int s = 0; s < kUnits; ++s) {
+            mbar_init(&u_full[s], 1);
+            mbar_init(&u_empty[s], 1 + kSoftWarps);  // the MMA warp and the softmax warps
         }
         mbar_init(&done_bar, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 9) {
+    if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
                      "r"(512)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    if (warp == 8 && lane == 0) {
+    if (warp == kCopyWarp && lane == 0) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(&pool_map) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&q_map) : "memory");
     }
@@ -195,21 +320,46 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the ring held the schedule's sums
     __syncthreads();
 
-    ChunkWalk<kKeys> wk;
-    wk.start(a, sh, rg);
-    auto tiles_of = [&]() { return wk.r.n - wk.k * sh.tok > tpt ? 2 : 1; };
+    // the copy thread walks the range; the others read what it has found
+    auto unit_wait = [&](uint32_t u) { return wait_bar(&u_full[u % kUnits], (u / kUnits) & 1u, a.err); };
 
-    if (warp >= 8) {
+    if (warp >= kSoftWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
-        if (warp == 8 && lane == 0) {
+        if (warp == kCopyWarp && lane == 0) {
             // ---- copies
             const uint32_t half_q = (uint32_t)(a.G * tpt) * 128u;
             uint32_t n = 0, u = 0;  // ring slots filled, units
             bool ok = true;
-            uint32_t blocks = 0;
-            for (; ok && wk.live(); wk.next(a, sh), ++u) {
-                if (!mbar_wait(&q_empty, (u & 1u) ^ 1u, a.err)) break;
-                const int two = tiles_of();
+            uint32_t blocks = 0, d = 0;
+            ChunkWalk<kKeys> wk;
+            auto publish = [&](bool live) {
+                if (!wait_bar(&u_empty[d % kUnits], ((d / kUnits) & 1u) ^ 1u, a.err)) return false;
+                UnitDesc& ud = unit_s[d % kUnits];
+                ud.nb = 0;
+                if (live) {
+                    ud.row0 = wk.r.row0;
+                    ud.n = wk.r.n;
+                    ud.kv = wk.r.kv;
+                    ud.g = wk.g;
+                    ud.tok0 = wk.k * sh.tok;
+                    ud.blk0 = wk.blk0;
+                    ud.nb = wk.blk1 - wk.blk0;
+                    ud.c0 = -1;
+                    if (!wk.whole()) {
+                        wk.pieces(rg, ud.c0, ud.c1);
+                        ud.slot0 = wk.slot(rg, ud.c0);  // (a later CTA's piece of the unit is its first: slot 2c)
+                    }
+                }
+                mbar_arrive(&u_full[d % kUnits]);
+                ++d;
+                return true;
+            };
+            for (wk.start(a, sh, rg); ok && wk.live(); wk.next(a, sh), ++u) {
+                if (!publish(true) || !wait_bar(&q_empty, (u & 1u) ^ 1u, a.err)) {
+                    ok = false;
+                    break;
+                }
+                const int two = wk.r.n - wk.k * sh.tok > tpt ? 2 : 1;
                 mbar_expect_tx(&q_full, 2u * half_q * two);
                 for (int t = 0; t < two; ++t)
                     for (int h = 0; h < 2; ++h)
@@ -238,7 +388,7 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
                     bad_s[blocks % kFlags] = bad;
                     for (int kv = 0; kv < 2; ++kv, ++n) {
                         const uint32_t st = n % kSlots;
-                        if (!mbar_wait(&kv_empty[st], ((n / kSlots) & 1u) ^ 1u, a.err)) {
+                        if (!wait_bar(&kv_empty[st], ((n / kSlots) & 1u) ^ 1u, a.err)) {
                             ok = false;
                             break;
                         }
@@ -255,52 +405,60 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
                     }
                 }
             }
+            if (ok) publish(false);
             // never leave with copies in flight
-            if (u > 0) mbar_wait(&q_full, (u - 1) & 1u, a.err);
-            for (uint32_t i = n > kSlots ? n - kSlots : 0; i < n; ++i) mbar_wait(&kv_full[i % kSlots], (i / kSlots) & 1u, a.err);
-        } else if (warp == 9 && lane == 0) {
+            if (u > 0) wait_bar(&q_full, (u - 1) & 1u, a.err);
+            for (uint32_t i = n > kSlots ? n - kSlots : 0; i < n; ++i) wait_bar(&kv_full[i % kSlots], (i / kSlots) & 1u, a.err);
+        } else if (warp == kMmaWarp) {
             // ---- MMAs
             constexpr uint32_t idesc_s = idesc_bf16(128, 128);
             constexpr uint32_t idesc_o = idesc_bf16(128, 128) | (1u << 16);  // V MN-major
-            const uint32_t q_addr = smem_u32(q_s), ring_addr = smem_u32(ring);
+            const uint32_t el = elect_one();
+            const uint64_t q_desc = smem_desc_sw128(smem_u32(q_s)), k_desc = smem_desc_sw128(smem_u32(ring)),
+                           val_desc = v_desc(smem_u32(ring));
             uint32_t n = 0, u = 0, pc[2] = {0, 0};  // ring slot of the unit's next K, units, P phases
             bool ok = true;
+            // descriptors count 16-byte units
             auto scores = [&](int t, uint32_t slot) {
-                const uint32_t qa = q_addr + (uint32_t)t * kQTile, ka = ring_addr + slot * kSlot;
+                const uint64_t qd = q_desc + (uint64_t)(t * (kQTile >> 4)), kd = k_desc + (uint64_t)(slot * (kSlot >> 4));
 #pragma unroll
                 for (int kk = 0; kk < kD / 16; ++kk) {
-                    const uint32_t off = (uint32_t)((kk >> 2) * kHalf + (kk & 3) * 32);
-                    mma_bf16(tmem + (uint32_t)t * 128u, smem_desc_sw128(qa + off), smem_desc_sw128(ka + off), idesc_s,
-                             kk > 0 ? 1u : 0u);
+                    const uint64_t off = (uint64_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
+                    mma_ss(el, tmem + (uint32_t)t * 128u, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
                 }
-                mma_commit(&s_full[t]);
+                commit_one(el, &s_full[t]);
             };
-            auto full = [&](uint32_t i) { return mbar_wait(&kv_full[i % kSlots], (i / kSlots) & 1u, a.err); };
-            for (; ok && wk.live(); wk.next(a, sh), ++u) {
-                const int two = tiles_of(), nb = wk.blk1 - wk.blk0;
-                if (!mbar_wait(&q_full, u & 1u, a.err) || !full(n)) break;
+            auto full = [&](uint32_t i) { return wait_bar(&kv_full[i % kSlots], (i / kSlots) & 1u, a.err); };
+            for (;; ++u) {
+                if (!unit_wait(u)) break;
+                const int nb = unit_s[u % kUnits].nb, two = unit_s[u % kUnits].n - unit_s[u % kUnits].tok0 > tpt ? 2 : 1;
+                __syncwarp();
+                if (el) mbar_arrive(&u_empty[u % kUnits]);
+                if (nb == 0 || !wait_bar(&q_full, u & 1u, a.err) || !full(n)) break;
                 tc_fence_after();
                 for (int t = 0; t < two; ++t) scores(t, n % kSlots);
-                mma_commit(&kv_empty[n % kSlots]);
-                if (nb == 1) mma_commit(&q_empty);
+                commit_one(el, &kv_empty[n % kSlots]);
+                if (nb == 1) commit_one(el, &q_empty);
                 for (int i = 0; ok && i < nb; ++i) {
                     const uint32_t vs = n + 2 * i + 1, kn = n + 2 * i + 2;
                     if (!full(vs)) {
                         ok = false;
                         break;
                     }
+                    const uint64_t vd = val_desc + (uint64_t)((vs % kSlots) * (kSlot >> 4));
                     for (int t = 0; t < two; ++t) {
-                        if (!mbar_wait(&p_full[t], pc[t] & 1u, a.err)) {
-                            ok = false;
-                            break;
-                        }
-                        ++pc[t];
-                        tc_fence_after();
-                        const uint32_t va = ring_addr + (vs % kSlots) * kSlot;
 #pragma unroll
-                        for (int kk = 0; kk < kKeys / 16; ++kk)
-                            mma_bf16_ts(tmem + 256u + (uint32_t)t * 128u, tmem + (uint32_t)t * 128u + kk * 8,
-                                        v_desc(va + kk * 2048), idesc_o, (i > 0 || kk > 0) ? 1u : 0u);
+                        for (int h = 0; h < 2; ++h) {  // the weights of the block's first 96 keys, then the rest
+                            ok = ok && wait_bar(&p_full[t][h], pc[t] & 1u, a.err);
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int kk = h ? kFirst / 16 : 0; kk < (h ? kKeys / 16 : kFirst / 16); ++kk)
+                                mma_ts(el, tmem + 256u + (uint32_t)t * 128u, tmem + (uint32_t)t * 128u + kk * 8,
+                                       vd + (uint64_t)(kk * (2048 >> 4)), idesc_o, (i > 0 || kk > 0) ? 1u : 0u);
+                        }
+                        if (!ok) break;
+                        ++pc[t];
                         if (i + 1 < nb) {
                             if (t == 0 && !full(kn)) {
                                 ok = false;
@@ -309,72 +467,78 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
                             tc_fence_after();
                             scores(t, kn % kSlots);
                         } else {
-                            mma_commit(&o_full[t]);
+                            commit_one(el, &o_full[t]);
                         }
                     }
                     if (!ok) break;
-                    if (i + 1 < nb) mma_commit(&kv_empty[kn % kSlots]);
-                    mma_commit(&kv_empty[vs % kSlots]);
-                    if (i + 2 == nb) mma_commit(&q_empty);  // the unit's last scores have been issued
+                    if (i + 1 < nb) commit_one(el, &kv_empty[kn % kSlots]);
+                    commit_one(el, &kv_empty[vs % kSlots]);
+                    if (i + 2 == nb) commit_one(el, &q_empty);  // the unit's last scores have been issued
                 }
+                if (!ok) break;
                 n += 2 * nb;
             }
-            mma_commit(&done_bar);
-            mbar_wait(&done_bar, 0u, a.err);
+            commit_one(el, &done_bar);
+            wait_bar(&done_bar, 0u, a.err);
+            __syncwarp();
         }
-        __syncwarp();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-        // ---- softmax and output of tile t
+        // ---- softmax and output of tile t, one thread per query vector
         const int t = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
-        const uint32_t s_addr = lane_base + (uint32_t)t * 128u, o_addr = lane_base + 256u + (uint32_t)t * 128u;
+        const uint32_t s_addr = lane_base + (uint32_t)(t * 128), o_addr = lane_base + 256u + (uint32_t)(t * 128);
         const float sl2 = a.scale * 1.4426950408889634f;
-        uint32_t n = 0, blocks = 0, sc = 0, units = 0;  // ring slots, blocks, S phases, units of this tile
+        uint32_t blocks = 0, sc = 0, units = 0;  // blocks (V of block j is in ring slot 2 j + 1), S phases, units of this tile
         bool alive = true;
-        for (; wk.live(); wk.next(a, sh)) {
-            const int nb = wk.blk1 - wk.blk0;
-            const int tok0 = wk.k * sh.tok + t * tpt;             // the tile's first token
-            const int nrow = min(tpt, wk.r.n - tok0) * a.G;
-            if (nrow <= 0) {  // only tile 1, the same decision as tiles_of()
-                n += 2 * nb;
+        for (uint32_t u = 0;; ++u) {
+            // the tile's warps go on or stop together: a wait that gave up in one of them alone would leave the
+            // others at a named barrier
+            if (!tile_agrees(t, unit_wait(u))) break;
+            const UnitDesc& ud = unit_s[u % kUnits];
+            const int nb = ud.nb;
+            if (nb == 0) break;
+            const int tok0 = ud.tok0 + t * tpt;                   // the tile's first token
+            const int nrow = min(tpt, ud.n - tok0) * a.G;
+            auto unit_done = [&]() {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&u_empty[u % kUnits]);
+            };
+            if (nrow <= 0) {  // only tile 1 of a short unit
                 blocks += nb;
+                unit_done();
                 continue;
             }
-            const int pos0 = wk.r.kv - wk.r.n + tok0, rt = r / a.G;
-            const int lim0 = chunk_visible(pos0, wk.r.kv, a.mask_block);  // the fewest keys a row of the tile sees
-            const int lim = chunk_visible(pos0 + rt, wk.r.kv, a.mask_block);
+            const int kv = ud.kv, rt = r / a.G;
+            const int lim0 = chunk_visible(kv - ud.n + tok0, kv, a.mask_block);  // the fewest keys a row of the tile sees
+            const int lim = chunk_visible(kv - ud.n + tok0 + rt, kv, a.mask_block);
+            int key0 = ud.blk0 * kKeys;
             float m = -CUDART_INF_F, l = 0.f;
-            for (int i = 0; i < nb; ++i, n += 2, ++blocks) {
-                const int key0 = (wk.blk0 + i) * kKeys;
-                alive = alive && mbar_wait(&s_full[t], sc & 1u, a.err);
+            for (int i = 0; i < nb; ++i, ++blocks, key0 += kKeys) {
+                alive = alive && wait_bar(&s_full[t], sc & 1u, a.err);
                 ++sc;
                 alive = __all_sync(0xffffffffu, alive);
                 if (!alive) continue;
                 tc_fence_after();
                 uint32_t s[128];
-                float mx0 = -CUDART_INF_F, mx1 = -CUDART_INF_F, mx2 = -CUDART_INF_F, mx3 = -CUDART_INF_F;
                 const uint32_t bad = bad_s[blocks % kFlags];
-                const bool masked = key0 + kKeys > lim0 || bad != 0;  // the same for the whole tile
-                tm_ld(s_addr, s);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    tm_wait(s + 32 * c);
-                    if (c < 3) tm_ld(s_addr + 32 * (c + 1), s + 32 * (c + 1));
-                    if (masked) {
-                        const int left = lim - key0 - 32 * c;
-                        const uint32_t b2 = bad >> (2 * c);
+                for (int c = 0; c < 4; ++c) tm_ld(s_addr + 32 * c, s + 32 * c);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (j >= left || ((b2 >> (j >> 4)) & 1u)) s[32 * c + j] = __float_as_uint(-CUDART_INF_F);
-                    }
+                for (int c = 0; c < 4; ++c) tm_wait(s + 32 * c);  // the first waits for all, the others tie the registers
+                if (key0 + kKeys > lim0 || bad != 0) {            // the same for the whole tile
+                    const int left = lim - key0;
 #pragma unroll
-                    for (int j = 0; j < 32; j += 8) {
-                        mx0 = fmaxf(fmaxf(mx0, __uint_as_float(s[32 * c + j])), __uint_as_float(s[32 * c + j + 1]));
-                        mx1 = fmaxf(fmaxf(mx1, __uint_as_float(s[32 * c + j + 2])), __uint_as_float(s[32 * c + j + 3]));
-                        mx2 = fmaxf(fmaxf(mx2, __uint_as_float(s[32 * c + j + 4])), __uint_as_float(s[32 * c + j + 5]));
-                        mx3 = fmaxf(fmaxf(mx3, __uint_as_float(s[32 * c + j + 6])), __uint_as_float(s[32 * c + j + 7]));
-                    }
+                    for (int j = 0; j < 128; ++j)
+                        if (j >= left || ((bad >> (j >> 4)) & 1u)) s[j] = __float_as_uint(-CUDART_INF_F);
+                }
+                float mx0 = -CUDART_INF_F, mx1 = -CUDART_INF_F, mx2 = -CUDART_INF_F, mx3 = -CUDART_INF_F;
+#pragma unroll
+                for (int j = 0; j < 128; j += 8) {
+                    mx0 = fmaxf(fmaxf(mx0, __uint_as_float(s[j])), __uint_as_float(s[j + 1]));
+                    mx1 = fmaxf(fmaxf(mx1, __uint_as_float(s[j + 2])), __uint_as_float(s[j + 3]));
+                    mx2 = fmaxf(fmaxf(mx2, __uint_as_float(s[j + 4])), __uint_as_float(s[j + 5]));
+                    mx3 = fmaxf(fmaxf(mx3, __uint_as_float(s[j + 6])), __uint_as_float(s[j + 7]));
                 }
                 const float cm = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * sl2;
                 float f = 1.f;
@@ -388,37 +552,22 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
                 if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll 1
                     for (int c = 0; c < kD; c += 32) {
-                        float v[32];
-                        tmem_ld32(o_addr + c, v);
                         uint32_t w[32];
+                        tm_ld(o_addr + c, w);
+                        tm_wait(w);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(v[j] * f);
+                        for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) * f);
                         tm_st(o_addr + c, w);
                     }
                     tm_wait_st();
                 }
-                const float mu = m == -CUDART_INF_F ? 0.f : m;
-                float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t pk[32];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const float p0 = ex2(fmaf(__uint_as_float(s[64 * h + 2 * j]), sl2, -mu));
-                        const float p1 = ex2(fmaf(__uint_as_float(s[64 * h + 2 * j + 1]), sl2, -mu));
-                        l0 += p0;
-                        l1 += p1;
-                        pk[j] = pack2(p0, p1);
-                    }
-                    tm_st(s_addr + 32 * h, pk);
-                }
-                l += l0 + l1;
                 // V rows of keys that do not exist may hold anything (a page's tail, an old copy): their weight
                 // is 0, so make them 0 as well
-                if (key0 + kKeys > wk.r.kv || bad != 0) {
-                    alive = __all_sync(0xffffffffu, mbar_wait(&kv_full[(n + 1) % kSlots], ((n + 1) / kSlots) & 1u, a.err));
-                    if (key0 + r >= wk.r.kv || ((bad >> (r >> 4)) & 1u)) {
-                        uint8_t* vr = ring + ((n + 1) % kSlots) * kSlot + r * 128;
+                if (key0 + kKeys > kv || bad != 0) {
+                    const uint32_t vs = 2 * blocks + 1;
+                    alive = __all_sync(0xffffffffu, wait_bar(&kv_full[vs % kSlots], (vs / kSlots) & 1u, a.err));
+                    if (key0 + r >= kv || ((bad >> (r >> 4)) & 1u)) {
+                        uint8_t* vr = ring + (vs % kSlots) * kSlot + r * 128;
 #pragma unroll
                         for (int c = 0; c < 8; ++c) {
                             *reinterpret_cast<uint4*>(vr + 16 * c) = make_uint4(0, 0, 0, 0);
@@ -426,18 +575,46 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
                         }
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    sync_tile(t);  // a first half handed over below may read rows that another warp zeroes
                 }
-                tm_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[t]);
+                const float mu = m == -CUDART_INF_F ? 0.f : m;
+                const uint64_t sl2x2 = f2(sl2, sl2), mux2 = f2(-mu, -mu);
+                uint64_t sum0 = 0, sum1 = 0;
+                uint32_t pk[64];
+                auto weights = [&](int j0, int j1) {
+#pragma unroll
+                    for (int j = j0; j < j1; ++j) {
+                        uint64_t x = fma2(f2(s[2 * j], s[2 * j + 1]), sl2x2, mux2);
+                        if ((j & 7) < kPolyOf8) exp2_poly_n<1>(&x);
+                        else x = exp2_mufu(x);
+                        if (j & 1) sum1 = add2(sum1, x);
+                        else sum0 = add2(sum0, x);
+                        pk[j] = pack2(__uint_as_float((uint32_t)x), __uint_as_float((uint32_t)(x >> 32)));
+                    }
+                };
+                auto hand_over = [&](int part) {
+                    tm_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_full[t][part]);
+                };
+                weights(0, 32);
+                tm_st(s_addr, pk);
+                weights(32, 48);
+                tm_st16(s_addr + 32, pk + 32);
+                hand_over(0);
+                weights(48, 64);
+                tm_st16(s_addr + 48, pk + 48);
+                hand_over(1);
+                const uint64_t sum = add2(sum0, sum1);
+                l += __uint_as_float((uint32_t)sum) + __uint_as_float((uint32_t)(sum >> 32));
             }
-            alive = alive && mbar_wait(&o_full[t], units & 1u, a.err);
+            alive = alive && wait_bar(&o_full[t], units & 1u, a.err);
             ++units;
             alive = __all_sync(0xffffffffu, alive);
             tc_fence_after();
-            bf16* dst = reinterpret_cast<bf16*>(a.out) + (long long)(wk.r.row0 + tok0 + rt) * a.out_stride +
-                        (wk.g * a.G + r - rt * a.G) * kD;
+            bf16* dst = reinterpret_cast<bf16*>(a.out) + (long long)(ud.row0 + tok0 + rt) * a.out_stride +
+                        (ud.g * a.G + r - rt * a.G) * kD;
             const bool live = r < nrow;
             auto store = [&](int c, const float (&v)[32], float inv) {  // 32 columns of the row
 #pragma unroll
@@ -446,7 +623,9 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
                         make_uint4(pack2(v[j] * inv, v[j + 1] * inv), pack2(v[j + 2] * inv, v[j + 3] * inv),
                                    pack2(v[j + 4] * inv, v[j + 5] * inv), pack2(v[j + 6] * inv, v[j + 7] * inv));
             };
-            if (wk.whole()) {
+            const int c0 = ud.c0, c1 = ud.c1, slot0 = ud.slot0;
+            unit_done();
+            if (c0 < 0) {
                 const float inv = l > 0.f ? 1.f / l : 0.f;
                 if (alive) {
 #pragma unroll 1
@@ -460,11 +639,9 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
                 continue;
             }
             // ---- a shared unit: leave the piece in scratch; the group that arrives last adds them in order
-            int c0, c1;
-            wk.pieces(rg, c0, c1);
             float4* po = reinterpret_cast<float4*>(a.part_o);
             float2* pm = reinterpret_cast<float2*>(a.part_ml);
-            auto piece = [&](int c) { return (size_t)wk.slot(rg, c) * 2 + t; };
+            auto piece = [&](int c) { return (size_t)(c == c0 ? slot0 : 2 * c) * 2 + t; };
             const size_t mine = piece(blockIdx.x);
             if (alive) {
 #pragma unroll 1
@@ -479,11 +656,11 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
             }
             __stcg(pm + mine * 128 + r, make_float2(m, l));
             __threadfence();
-            sync_group(t);
+            sync_tile(t);
             if (r == 0)
                 last_s[t] = atomicInc(reinterpret_cast<unsigned*>(a.counters) + 2 * c0 + t, (unsigned)(c1 - c0)) ==
                             (unsigned)(c1 - c0);
-            sync_group(t);
+            sync_tile(t);
             if (!last_s[t]) continue;
             __threadfence();
             float mm = -CUDART_INF_F, ll = 0.f;
@@ -519,7 +696,7 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
 // Query rows as (64-column half, head, row): one box is G heads of 128 / G tokens, 128-byte rows, swizzled.
