@@ -40,17 +40,17 @@ using tc::tma_load_2d;
 using tc::tmem_ld32;
 
 constexpr int kD = 128;
-constexpr int kKeys = 128;                    // keys per block
-constexpr int kHalf = 128 * 128;              // [128 rows][64 columns] bf16: 16 KB
-constexpr int kSlot = 2 * kHalf;              // K or V of one block: 32 KB
-constexpr int kSlots = 4;
-constexpr int kQTile = 2 * kHalf;             // one query tile: 32 KB
+constexpr int kKeys = 64;                     // keys per block
+constexpr int kHalf = kKeys * 128;            // [64 keys][64 columns] bf16: 8 KB
+constexpr int kSlot = 2 * kHalf;              // K or V of one block: 16 KB
+constexpr int kSlots = 9;
+constexpr int kQHalf = 128 * 128;             // [128 query vectors][64 columns]
+constexpr int kQTile = 2 * kQHalf;            // one query tile: 32 KB
 constexpr int kSmem = 2 * kQTile + kSlots * kSlot + 1024;
 constexpr int kSoftWarps = 8;                 // 4 per tile: one thread per query vector
-constexpr int kFirst = 96;                    // keys of a block whose weights are handed over first
-constexpr int kTileThreads = 32 * kSoftWarps + 128;  // then one warp for the copies and one for the MMAs
-constexpr int kCopyWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
-constexpr int kFlags = 8;                     // bad-page flags, one per block in flight
+constexpr int kTileThreads = 32 * kSoftWarps + 128;  // then one warp for the copies and one per tile for the MMAs
+constexpr int kCopyWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;  // tile t: warp kMmaWarp + t
+constexpr int kFlags = 16;                    // bad-page flags, one per block in flight
 constexpr int kUnits = 4;                     // unit descriptors in flight
 constexpr float kRaise = 8.f;
 constexpr float kExp1 = 0.69328290f, kExp2 = 0.24221095f, kExp3 = 0.05500893f;
@@ -145,14 +145,6 @@ __device__ __forceinline__ void tm_st(uint32_t taddr, const uint32_t* r) {
           "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
           "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
           "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
-}
-__device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t* r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
-        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -268,8 +260,8 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* q_s = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* ring = q_s + 2 * kQTile;
-    __shared__ __align__(8) uint64_t q_full, q_empty, kv_full[kSlots], kv_empty[kSlots], s_full[2], p_full[2][2],
-        o_full[2], done_bar, u_full[kUnits], u_empty[kUnits];
+    __shared__ __align__(8) uint64_t q_full, q_empty, kv_full[kSlots], kv_empty[kSlots], s_full[2][2],
+        p_full[2][2], o_full[2], done_bar[2], u_full[kUnits], u_empty[kUnits];
     __shared__ UnitDesc unit_s[kUnits];
     __shared__ uint32_t bad_s[kFlags];  // per block: 16-key groups whose page id is invalid
     __shared__ uint32_t tmem_slot;
@@ -280,22 +272,23 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         mbar_init(&q_full, 1);
-        mbar_init(&q_empty, 1);
+        mbar_init(&q_empty, 2);  // both tiles' MMA warps
         for (int s = 0; s < kSlots; ++s) {
             mbar_init(&kv_full[s], 1);
-            mbar_init(&kv_empty[s], 1);
+            mbar_init(&kv_empty[s], 2);
         }
         for (int t = 0; t < 2; ++t) {
-            mbar_init(&s_full[t], 1);
-            mbar_init(&p_full[t][0], 4);  // one arrival per softmax warp
-            mbar_init(&p_full[t][1], 4);
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(&s_full[t][b], 1);
+                mbar_init(&p_full[t][b], 4);  // one arrival per softmax warp
+            }
             mbar_init(&o_full[t], 1);
+            mbar_init(&done_bar[t], 1);
         }
         for (int s = 0; s < kUnits; ++s) {
             mbar_init(&u_full[s], 1);
-            mbar_init(&u_empty[s], 1 + kSoftWarps);  // the MMA warp and the softmax warps
+            mbar_init(&u_empty[s], 2 + kSoftWarps);  // the MMA and the softmax warps
         }
-        mbar_init(&done_bar, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kMmaWarp) {
@@ -363,7 +356,7 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
                 mbar_expect_tx(&q_full, 2u * half_q * two);
                 for (int t = 0; t < two; ++t)
                     for (int h = 0; h < 2; ++h)
-                        tma_load_3d(&q_map, &q_full, q_s + t * kQTile + h * kHalf, h * 64, wk.g * a.G,
+                        tma_load_3d(&q_map, &q_full, q_s + t * kQTile + h * kQHalf, h * 64, wk.g * a.G,
                                     wk.r.row0 + wk.k * sh.tok + t * tpt);
                 const int32_t* pt = a.page_table + (size_t)wk.b * a.max_pages;
                 for (int blk = wk.blk0; ok && blk < wk.blk1; ++blk, ++blocks) {
@@ -409,77 +402,82 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
             // never leave with copies in flight
             if (u > 0) wait_bar(&q_full, (u - 1) & 1u, a.err);
             for (uint32_t i = n > kSlots ? n - kSlots : 0; i < n; ++i) wait_bar(&kv_full[i % kSlots], (i / kSlots) & 1u, a.err);
-        } else if (warp == kMmaWarp) {
-            // ---- MMAs
-            constexpr uint32_t idesc_s = idesc_bf16(128, 128);
-            constexpr uint32_t idesc_o = idesc_bf16(128, 128) | (1u << 16);  // V MN-major
+        } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+            // ---- MMAs of tile t: S(j + 2) goes out behind P V(j), so the scores of the next block are ready when the
+            // softmax has finished this one.  (One warp for both tiles left the tensor core idle while it waited
+            // and committed for the other tile.)
+            const int t = warp - kMmaWarp;
+            constexpr uint32_t idesc_s = idesc_bf16(128, kKeys);
+            constexpr uint32_t idesc_o = idesc_bf16(128, kD) | (1u << 16);  // V MN-major
             const uint32_t el = elect_one();
-            const uint64_t q_desc = smem_desc_sw128(smem_u32(q_s)), k_desc = smem_desc_sw128(smem_u32(ring)),
+            const uint64_t q_desc = smem_desc_sw128(smem_u32(q_s + t * kQTile)), k_desc = smem_desc_sw128(smem_u32(ring)),
                            val_desc = v_desc(smem_u32(ring));
-            uint32_t n = 0, u = 0, pc[2] = {0, 0};  // ring slot of the unit's next K, units, P phases
-            bool ok = true;
+            const uint32_t s_col = tmem + (uint32_t)t * 128u, o_col = tmem + 256u + (uint32_t)t * 128u;
+            uint32_t n = 0, sc = 0, pc = 0;  // ring slot of the unit's first K; blocks of S, of P
             // descriptors count 16-byte units
-            auto scores = [&](int t, uint32_t slot) {
-                const uint64_t qd = q_desc + (uint64_t)(t * (kQTile >> 4)), kd = k_desc + (uint64_t)(slot * (kSlot >> 4));
+            auto scores = [&](uint32_t slot) {
+                const uint64_t kd = k_desc + (uint64_t)(slot * (kSlot >> 4));
+                const uint32_t d = s_col + (sc & 1u) * 64u;
 #pragma unroll
-                for (int kk = 0; kk < kD / 16; ++kk) {
-                    const uint64_t off = (uint64_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
-                    mma_ss(el, tmem + (uint32_t)t * 128u, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
-                }
-                commit_one(el, &s_full[t]);
+                for (int kk = 0; kk < kD / 16; ++kk)
+                    mma_ss(el, d, q_desc + (uint64_t)(((kk >> 2) * kQHalf + (kk & 3) * 32) >> 4),
+                           kd + (uint64_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4), idesc_s, kk > 0 ? 1u : 0u);
+                commit_one(el, &s_full[t][sc & 1u]);
+                commit_one(el, &kv_empty[slot]);
+                ++sc;
             };
             auto full = [&](uint32_t i) { return wait_bar(&kv_full[i % kSlots], (i / kSlots) & 1u, a.err); };
-            for (;; ++u) {
+            bool ok = true;
+            for (uint32_t u = 0; ok; ++u) {
                 if (!unit_wait(u)) break;
-                const int nb = unit_s[u % kUnits].nb, two = unit_s[u % kUnits].n - unit_s[u % kUnits].tok0 > tpt ? 2 : 1;
+                const int nb = unit_s[u % kUnits].nb;
+                const bool mine = t == 0 || unit_s[u % kUnits].n - unit_s[u % kUnits].tok0 > tpt;
                 __syncwarp();
                 if (el) mbar_arrive(&u_empty[u % kUnits]);
-                if (nb == 0 || !wait_bar(&q_full, u & 1u, a.err) || !full(n)) break;
-                tc_fence_after();
-                for (int t = 0; t < two; ++t) scores(t, n % kSlots);
-                commit_one(el, &kv_empty[n % kSlots]);
-                if (nb == 1) commit_one(el, &q_empty);
-                for (int i = 0; ok && i < nb; ++i) {
-                    const uint32_t vs = n + 2 * i + 1, kn = n + 2 * i + 2;
-                    if (!full(vs)) {
-                        ok = false;
-                        break;
+                if (nb == 0) break;
+                if (!mine) {  // a short unit's second tile: give its ring slots back as they come
+                    if (el) mbar_arrive(&q_empty);
+                    for (int j = 0; ok && j < 2 * nb; ++j, ++n) {
+                        ok = full(n);
+                        __syncwarp();
+                        if (ok && el) mbar_arrive(&kv_empty[n % kSlots]);
                     }
-                    const uint64_t vd = val_desc + (uint64_t)((vs % kSlots) * (kSlot >> 4));
-                    for (int t = 0; t < two; ++t) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {  // the weights of the block's first 96 keys, then the rest
-                            ok = ok && wait_bar(&p_full[t][h], pc[t] & 1u, a.err);
-                            if (!ok) break;
-                            tc_fence_after();
-#pragma unroll
-                            for (int kk = h ? kFirst / 16 : 0; kk < (h ? kKeys / 16 : kFirst / 16); ++kk)
-                                mma_ts(el, tmem + 256u + (uint32_t)t * 128u, tmem + (uint32_t)t * 128u + kk * 8,
-                                       vd + (uint64_t)(kk * (2048 >> 4)), idesc_o, (i > 0 || kk > 0) ? 1u : 0u);
-                        }
-                        if (!ok) break;
-                        ++pc[t];
-                        if (i + 1 < nb) {
-                            if (t == 0 && !full(kn)) {
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after();
-                            scores(t, kn % kSlots);
-                        } else {
-                            commit_one(el, &o_full[t]);
-                        }
-                    }
-                    if (!ok) break;
-                    if (i + 1 < nb) commit_one(el, &kv_empty[kn % kSlots]);
-                    commit_one(el, &kv_empty[vs % kSlots]);
-                    if (i + 2 == nb) commit_one(el, &q_empty);  // the unit's last scores have been issued
+                    continue;
                 }
-                if (!ok) break;
+                if (!wait_bar(&q_full, u & 1u, a.err)) break;
+                for (int j = 0; ok && j < 2 && j < nb; ++j) {
+                    ok = full(n + 2 * j);
+                    if (!ok) break;
+                    tc_fence_after();
+                    scores((n + 2 * j) % kSlots);
+                }
+                if (nb <= 2) commit_one(el, &q_empty);
+                for (int j = 0; ok && j < nb; ++j) {
+                    const uint32_t vs = n + 2 * j + 1, kn = n + 2 * j + 4, b = pc & 1u;
+                    const bool more = j + 2 < nb;
+                    ok = full(vs) && wait_bar(&p_full[t][b], (pc >> 1) & 1u, a.err);
+                    if (!ok) break;
+                    ++pc;
+                    tc_fence_after();
+                    const uint64_t vd = val_desc + (uint64_t)((vs % kSlots) * (kSlot >> 4));
+#pragma unroll
+                    for (int kk = 0; kk < kKeys / 16; ++kk)
+                        mma_ts(el, o_col, s_col + b * 64u + kk * 8, vd + (uint64_t)(kk * (2048 >> 4)), idesc_o,
+                               (j > 0 || kk > 0) ? 1u : 0u);
+                    commit_one(el, &o_full[t]);
+                    commit_one(el, &kv_empty[vs % kSlots]);
+                    if (more) {
+                        ok = full(kn);
+                        if (!ok) break;
+                        tc_fence_after();
+                        scores(kn % kSlots);
+                    }
+                    if (j + 3 == nb) commit_one(el, &q_empty);  // the unit's last scores have been issued
+                }
                 n += 2 * nb;
             }
-            commit_one(el, &done_bar);
-            wait_bar(&done_bar, 0u, a.err);
+            commit_one(el, &done_bar[t]);
+            wait_bar(&done_bar[t], 0u, a.err);
             __syncwarp();
         }
     } else {
@@ -489,7 +487,7 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
         const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t s_addr = lane_base + (uint32_t)(t * 128), o_addr = lane_base + 256u + (uint32_t)(t * 128);
         const float sl2 = a.scale * 1.4426950408889634f;
-        uint32_t blocks = 0, sc = 0, units = 0;  // blocks (V of block j is in ring slot 2 j + 1), S phases, units of this tile
+        uint32_t blocks = 0, sc = 0;  // blocks (V of block j is in ring slot 2 j + 1), blocks of this tile
         bool alive = true;
         for (uint32_t u = 0;; ++u) {
             // the tile's warps go on or stop together: a wait that gave up in one of them alone would leave the
@@ -515,26 +513,28 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
             int key0 = ud.blk0 * kKeys;
             float m = -CUDART_INF_F, l = 0.f;
             for (int i = 0; i < nb; ++i, ++blocks, key0 += kKeys) {
-                alive = alive && wait_bar(&s_full[t], sc & 1u, a.err);
+                const uint32_t b = sc & 1u;
+                alive = alive && wait_bar(&s_full[t][b], (sc >> 1) & 1u, a.err);
                 ++sc;
                 alive = __all_sync(0xffffffffu, alive);
                 if (!alive) continue;
                 tc_fence_after();
-                uint32_t s[128];
+                uint32_t s[64];
+                const uint32_t sb = s_addr + 64 * b;
                 const uint32_t bad = bad_s[blocks % kFlags];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tm_ld(s_addr + 32 * c, s + 32 * c);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tm_wait(s + 32 * c);  // the first waits for all, the others tie the registers
-                if (key0 + kKeys > lim0 || bad != 0) {            // the same for the whole tile
+                tm_ld(sb, s);
+                tm_ld(sb + 32, s + 32);
+                tm_wait(s);       // waits for both,
+                tm_wait(s + 32);  // this one ties the registers
+                if (key0 + kKeys > lim0 || bad != 0) {  // the same for the whole tile
                     const int left = lim - key0;
 #pragma unroll
-                    for (int j = 0; j < 128; ++j)
+                    for (int j = 0; j < 64; ++j)
                         if (j >= left || ((bad >> (j >> 4)) & 1u)) s[j] = __float_as_uint(-CUDART_INF_F);
                 }
                 float mx0 = -CUDART_INF_F, mx1 = -CUDART_INF_F, mx2 = -CUDART_INF_F, mx3 = -CUDART_INF_F;
 #pragma unroll
-                for (int j = 0; j < 128; j += 8) {
+                for (int j = 0; j < 64; j += 8) {
                     mx0 = fmaxf(fmaxf(mx0, __uint_as_float(s[j])), __uint_as_float(s[j + 1]));
                     mx1 = fmaxf(fmaxf(mx1, __uint_as_float(s[j + 2])), __uint_as_float(s[j + 3]));
                     mx2 = fmaxf(fmaxf(mx2, __uint_as_float(s[j + 4])), __uint_as_float(s[j + 5]));
@@ -550,6 +550,10 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
                     m = cm;
                 }
                 if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+                    // O has to hold the previous block's P V (its barrier is at most one phase past this one, since
+                    // this block's P V waits for the P below)
+                    alive = __all_sync(0xffffffffu, wait_bar(&o_full[t], (sc - 2) & 1u, a.err));
+                    tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < kD; c += 32) {
                         uint32_t w[32];
@@ -566,51 +570,39 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
                 if (key0 + kKeys > kv || bad != 0) {
                     const uint32_t vs = 2 * blocks + 1;
                     alive = __all_sync(0xffffffffu, wait_bar(&kv_full[vs % kSlots], (vs / kSlots) & 1u, a.err));
-                    if (key0 + r >= kv || ((bad >> (r >> 4)) & 1u)) {
-                        uint8_t* vr = ring + (vs % kSlots) * kSlot + r * 128;
+                    const int key = r & 63;
+                    if (key0 + key >= kv || ((bad >> (key >> 4)) & 1u)) {
+                        uint8_t* vr = ring + (vs % kSlots) * kSlot + (r >> 6) * kHalf + key * 128;
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            *reinterpret_cast<uint4*>(vr + 16 * c) = make_uint4(0, 0, 0, 0);
-                            *reinterpret_cast<uint4*>(vr + kHalf + 16 * c) = make_uint4(0, 0, 0, 0);
-                        }
+                        for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(vr + 16 * c) = make_uint4(0, 0, 0, 0);
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    sync_tile(t);  // a first half handed over below may read rows that another warp zeroes
                 }
                 const float mu = m == -CUDART_INF_F ? 0.f : m;
                 const uint64_t sl2x2 = f2(sl2, sl2), mux2 = f2(-mu, -mu);
                 uint64_t sum0 = 0, sum1 = 0;
-                uint32_t pk[64];
-                auto weights = [&](int j0, int j1) {
+                uint32_t pk[32];
 #pragma unroll
-                    for (int j = j0; j < j1; ++j) {
-                        uint64_t x = fma2(f2(s[2 * j], s[2 * j + 1]), sl2x2, mux2);
-                        if ((j & 7) < kPolyOf8) exp2_poly_n<1>(&x);
-                        else x = exp2_mufu(x);
-                        if (j & 1) sum1 = add2(sum1, x);
-                        else sum0 = add2(sum0, x);
-                        pk[j] = pack2(__uint_as_float((uint32_t)x), __uint_as_float((uint32_t)(x >> 32)));
-                    }
-                };
-                auto hand_over = [&](int part) {
-                    tm_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&p_full[t][part]);
-                };
-                weights(0, 32);
-                tm_st(s_addr, pk);
-                weights(32, 48);
-                tm_st16(s_addr + 32, pk + 32);
-                hand_over(0);
-                weights(48, 64);
-                tm_st16(s_addr + 48, pk + 48);
-                hand_over(1);
+                for (int j = 0; j < 32; ++j) {
+                    uint64_t x = fma2(f2(s[2 * j], s[2 * j + 1]), sl2x2, mux2);
+                    if ((j & 7) < kPolyOf8) exp2_poly_n<1>(&x);
+                    else x = exp2_mufu(x);
+                    if (j & 1) sum1 = add2(sum1, x);
+                    else sum0 = add2(sum0, x);
+                    pk[j] = pack2(__uint_as_float((uint32_t)x), __uint_as_float((uint32_t)(x >> 32)));
+                }
+                tm_st(sb, pk);
+                tm_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[t][b]);
                 const uint64_t sum = add2(sum0, sum1);
                 l += __uint_as_float((uint32_t)sum) + __uint_as_float((uint32_t)(sum >> 32));
             }
-            alive = alive && wait_bar(&o_full[t], units & 1u, a.err);
-            ++units;
+            // the last scores only promise the P V two blocks back; a parity wait must not be two phases ahead, so
+            // wait for the last but one as well
+            alive = alive && (sc < 2 || wait_bar(&o_full[t], (sc - 2) & 1u, a.err)) &&
+                    wait_bar(&o_full[t], (sc - 1) & 1u, a.err);
             alive = __all_sync(0xffffffffu, alive);
             tc_fence_after();
             bf16* dst = reinterpret_cast<bf16*>(a.out) + (long long)(ud.row0 + tok0 + rt) * a.out_stride +
