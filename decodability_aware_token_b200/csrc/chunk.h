@@ -42,8 +42,10 @@ struct ChunkAttnDev {
     int* err;
 };
 // bf16 models: requests of at most kChunkFewRows query vectors per KV head (single tokens) and the others
-constexpr int kChunkFewRows = 8;
+constexpr int kChunkFewRows = 16;
 constexpr int kChunkTileRows = 256;  // query vectors per unit of the tile kernel
+int launch_chunk_attention_few(const ChunkAttnDev& a, int sms, cudaStream_t s);
+bool configure_chunk_attention_few();
 int launch_chunk_attention_tile(const ChunkAttnDev& a, int sms, cudaStream_t s);
 bool configure_chunk_attention_tile();
 

@@ -116,7 +116,8 @@ int focus_chunk_init(const focus_chunk_cfg* cfg, const focus_chunk_limits* lim, 
         freq[i] = pow((double)cfg->rope_theta, -2.0 * i / cfg->head_dim) / 3.14159265358979323846;
     if (cudaMemcpy(c->freq_over_pi, freq, (size_t)cfg->head_dim / 2 * 8, cudaMemcpyHostToDevice) != cudaSuccess ||
         cudaMemset(c->err, 0, l.part_ml - l.words) != cudaSuccess || !configure_chunk_plan_kernel() ||
-        !configure_chunk_attention_simt() || !configure_chunk_attention_tile() || cudaDeviceSynchronize() != cudaSuccess) {
+        !configure_chunk_attention_simt() || !configure_chunk_attention_few() ||
+        !configure_chunk_attention_tile() || cudaDeviceSynchronize() != cudaSuccess) {
         (void)cudaGetLastError();
         cudaFree(c->ws);
         delete c;
@@ -251,7 +252,8 @@ int focus_chunk_attention(focus_chunk_ctx* c, const focus_chunk_attn* p, void* s
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     int n;
     if (bf) {
-        n = launch_chunk_attention_simt<bf16, 128>(a, c->sms, s);
+        // each kernel serves the requests on its side of kChunkFewRows query vectors and skips the others
+        n = a.G <= kChunkFewRows ? launch_chunk_attention_few(a, c->sms, s) : 0;
         if (n >= 0 && (int64_t)a.max_new * a.G > kChunkFewRows) n = launch_chunk_attention_tile(a, c->sms, s);
     } else {
         n = c->cfg.head_dim == 64 ? launch_chunk_attention_simt<float, 64>(a, c->sms, s)

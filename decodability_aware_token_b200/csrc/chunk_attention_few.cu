@@ -1,0 +1,418 @@
+// bf16 attention of requests with at most kChunkFewRows query vectors per KV head (single tokens, a few
+// speculative ones) over the paged cache, on mma.sync m16n8k16: with 16 rows the tensor work is a fraction of the
+// copy time whatever the instruction, and fragments in registers need no TMEM round trip per block.
+//
+// Bound by memory: each cached key and value is read once (64 Hkv d bytes ... per 16-key step 8 KB), so the design
+// is a copy that never stops.  One CTA per SM walks its equal share of the batch's key blocks (chunk_work.cuh);
+// one warp issues the pages of 64-key blocks by TMA into a ring of six 32 KB stages and runs on across unit
+// ends; eight warps consume, four per block, 16 keys each.  A warp keeps its own running maximum, denominator
+// and 16 x 128 output, so nothing is exchanged while a unit lasts; the eight are joined in shared memory at its
+// end, and pieces of a unit that spans CTAs are joined by the CTA that finishes last, in block order.
+//
+// Weights are rounded to bf16 for the product with V (relative 2^-9 each, as the values' own type); maxima,
+// denominators and outputs are float32.  The running maximum is raised only by more than 2^8.
+#include <math_constants.h>
+
+#include "chunk_pipe.cuh"
+
+namespace focus {
+namespace {
+
+constexpr int kD = 128;
+constexpr int kKeys = 64;
+constexpr int kHalf = kKeys * 128;           // [64 keys][64 columns] bf16
+constexpr int kStage = 4 * kHalf;            // K lo, K hi, V lo, V hi: 32 KB
+constexpr int kStages = 6;
+constexpr int kRows = kChunkFewRows;
+static_assert(kRows == 16, "one m16 tile");
+constexpr int kConsumers = 8;
+constexpr int kFewThreads = 32 * (kConsumers + 1);
+constexpr int kMergeStride = kD + 4;         // floats per row of the join buffers: rows 4 banks apart
+constexpr int kMergeF = kRows * kMergeStride;
+constexpr int kFewSmem = kStages * kStage + 2 * kMergeF * 4 + 1024;
+static_assert(kFewSmem <= 216 * 1024, "shared memory");
+static_assert(kChunkMaxRequests * 8 <= kStages * kStage, "the schedule's sums fit in the ring");
+constexpr float kRaise = 8.f;
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ex2f(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+__global__ void __launch_bounds__(kFewThreads, 1)
+chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev a) {
+    pdl_trigger();
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float* join = reinterpret_cast<float*>(ring + kStages * kStage);  // two [16][kMergeStride] buffers
+    __shared__ __align__(8) uint64_t full[kStages], empty[kStages], u_full[kUnits], u_empty[kUnits];
+    __shared__ UnitDesc unit_s[kUnits];
+    __shared__ uint32_t bad_s[kStages];       // 16-key groups of the stage whose page id is invalid
+    __shared__ ChunkRange rg;
+    __shared__ long long red[32];
+    __shared__ float jm[kConsumers][kRows], jl[kConsumers][kRows];
+    __shared__ int last_s;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 4);  // the four warps that consume the block
+        }
+        for (int s = 0; s < kUnits; ++s) {
+            mbar_init(&u_full[s], 1);
+            mbar_init(&u_empty[s], kConsumers);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&pool_map) : "memory");
+    }
+    pdl_wait();
+    const ChunkShape sh{kRows / a.G, 0, kRows};
+    chunk_schedule<kKeys>(a, sh, 2, reinterpret_cast<long long*>(ring), red, &rg);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the ring held the schedule's sums
+    __syncthreads();
+
+    if (warp == kConsumers) {
+        // ---- copies: the whole warp walks; lane i issues page i / 4's K lo, K hi, V lo, V hi copy number i % 4
+        const int ppb = kKeys / a.S;  // pages per block
+        uint32_t n = 0, d = 0;        // stages filled, units described
+        bool ok = true;
+        ChunkWalk<kKeys> wk;
+        auto publish = [&](bool live) {
+            bool got = wait_bar(&u_empty[d % kUnits], ((d / kUnits) & 1u) ^ 1u, a.err);
+            got = __all_sync(0xffffffffu, got);
+            if (!got) return false;
+            if (lane == 0) {
+                describe(unit_s[d % kUnits], wk, rg, sh, live);
+                mbar_arrive(&u_full[d % kUnits]);
+            }
+            __syncwarp();
+            ++d;
+            return true;
+        };
+        for (wk.start(a, sh, rg); ok && wk.live(); wk.next(a, sh)) {
+            ok = publish(true);
+            const int32_t* pt = a.page_table + (size_t)wk.b * a.max_pages;
+            int ahead0 = -1, ahead = 0;  // page ids of table entries ahead0 + lane
+            for (int blk = wk.blk0; ok && blk < wk.blk1; ++blk, ++n) {
+                const int key0 = blk * kKeys, p0 = key0 / a.S;
+                const int np = (max(0, min(kKeys, wk.r.kv - key0)) + a.S - 1) / a.S;
+                if (ahead0 < 0 || p0 + ppb > ahead0 + 32) {
+                    ahead0 = p0;
+                    ahead = p0 + lane < a.max_pages ? pt[p0 + lane] : -1;
+                }
+                const int page = __shfl_sync(0xffffffffu, ahead, (p0 - ahead0 + (lane >> 2)) & 31);
+                const bool mine = (lane >> 2) < np;
+                const bool good = mine && page >= 0 && page < a.n_pages;
+                const uint32_t good_m = __ballot_sync(0xffffffffu, good), bad_m = __ballot_sync(0xffffffffu, mine && !good);
+                uint32_t bad = 0;
+                for (int p = 0; p < np; ++p)
+                    if ((bad_m >> (4 * p)) & 1u) bad |= ((1u << (a.S / 16)) - 1u) << (p * (a.S / 16));
+                const uint32_t st = n % kStages;
+                ok = __all_sync(0xffffffffu, wait_bar(&empty[st], ((n / kStages) & 1u) ^ 1u, a.err));
+                if (!ok) break;
+                if (lane == 0) {
+                    if (bad) raise_err(a.err, FOCUS_DEVERR_PAGE_ID);
+                    bad_s[st] = bad;
+                    mbar_expect_tx(&full[st], (uint32_t)__popc(good_m) * (uint32_t)a.S * 128u);
+                }
+                __syncwarp();
+                if (good) {
+                    const int kv = (lane >> 1) & 1, h = lane & 1;
+                    const int row = (int)(((((long long)page * a.L + a.layer) * 2 + kv) * a.Hkv + wk.g) * a.S);
+                    tma_load_2d(&pool_map, &full[st], ring + st * kStage + (2 * kv + h) * kHalf + (lane >> 2) * a.S * 128,
+                                h * 64, row);
+                }
+                __syncwarp();
+            }
+        }
+        if (ok) publish(false);
+        // never leave with copies in flight
+        for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i) wait_bar(&full[i % kStages], (i / kStages) & 1u, a.err);
+        return;
+    }
+
+    // ---- consumers: warps 0-3 take the even blocks of the CTA's walk, 4-7 the odd ones
+    const int grp = warp >> 2, ks = (warp & 3) * 16;  // this warp's 16 keys of a block
+    const int g4 = lane >> 2, t4 = lane & 3;          // fragment row, column pair
+    const float sl2 = a.scale * 1.4426950408889634f;
+    // ldmatrix row addresses within a stage: K (keys x 32 columns a step), V transposed (16 keys x 16 columns)
+    const int krow = ks + (lane & 7), kc = lane >> 3;               // + 8 keys per n tile, 16-byte column kc
+    const int vrow = ks + (lane & 7) + ((lane >> 3) & 1) * 8, vc = lane >> 4;
+    uint32_t n = 0;
+    bool alive = true;
+    for (uint32_t u = 0;; ++u) {
+        // the eight warps go on or stop together: a wait that gave up in one of them alone would leave the others
+        // at a named barrier
+        if (!all_agree<32 * kConsumers>(1, wait_bar(&u_full[u % kUnits], (u / kUnits) & 1u, a.err))) break;
+        const UnitDesc& ud = unit_s[u % kUnits];
+        const int nb = ud.nb;
+        if (nb == 0) break;
+        const int nrow = min(sh.tok, ud.n - ud.tok0) * a.G, kv = ud.kv;
+        const int pos0 = kv - ud.n + ud.tok0;
+        // query fragments: rows g4 and g4 + 8, columns 16 s + 2 t4 (+ 1) and + 8
+        uint32_t q[8][4];
+        const bf16* qp = reinterpret_cast<const bf16*>(a.q) + (long long)(ud.row0 + ud.tok0) * a.q_stride + ud.g * a.G * kD;
+        auto q_row = [&](int r) { return qp + (long long)(r / a.G) * a.q_stride + (r % a.G) * kD + 2 * t4; };
+        const bool in0 = g4 < nrow, in1 = g4 + 8 < nrow;
+        const bf16 *q0 = q_row(g4), *q1 = q_row(g4 + 8);
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            q[s][0] = in0 ? *reinterpret_cast<const uint32_t*>(q0 + 16 * s) : 0u;
+            q[s][1] = in1 ? *reinterpret_cast<const uint32_t*>(q1 + 16 * s) : 0u;
+            q[s][2] = in0 ? *reinterpret_cast<const uint32_t*>(q0 + 16 * s + 8) : 0u;
+            q[s][3] = in1 ? *reinterpret_cast<const uint32_t*>(q1 + 16 * s + 8) : 0u;
+        }
+        const int lim0 = in0 ? chunk_visible(pos0 + g4 / a.G, kv, a.mask_block) : 0;
+        const int lim1 = in1 ? chunk_visible(pos0 + (g4 + 8) / a.G, kv, a.mask_block) : 0;
+        const int lim_all = chunk_visible(pos0, kv, a.mask_block);  // the fewest keys a row sees
+        float m0 = -CUDART_INF_F, m1 = -CUDART_INF_F, l0 = 0.f, l1 = 0.f;
+        float o[16][4];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+
+        for (int i = 0; i < nb; ++i, ++n) {
+            if ((int)(n & 1u) != grp) continue;
+            const uint32_t st = n % kStages;
+            alive = __all_sync(0xffffffffu, alive && wait_bar(&full[st], (n / kStages) & 1u, a.err));
+            if (!alive) continue;
+            const int key0 = (ud.blk0 + i) * kKeys + ks;
+            const uint32_t bad = (bad_s[st] >> (ks >> 4)) & 1u;
+            uint8_t* stage = ring + st * kStage;
+            const uint32_t kb = smem_u32(stage), vb = kb + 2 * kHalf;
+            float s[2][4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
+            // S: 16 rows x 16 keys, 128 columns
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {  // 32 columns: 16-byte chunks 4 c .. 4 c + 3 of 16
+                const int ch = 4 * (c & 1) + kc;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int row = krow + 8 * j;
+                    uint32_t b[4];
+                    ldsm4(b, kb + (c >> 1) * kHalf + row * 128 + ((ch ^ (row & 7)) << 4));
+                    mma16816(s[j], q[2 * c], b[0], b[1]);
+                    mma16816(s[j], q[2 * c + 1], b[2], b[3]);
+                }
+            }
+            if (key0 + 16 > lim_all || bad) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int key = key0 + 8 * j + 2 * t4 + (e & 1);
+                        if (key >= (e < 2 ? lim0 : lim1) || bad) s[j][e] = -CUDART_INF_F;
+                    }
+            }
+            // V rows of keys that do not exist may hold anything: their weight is 0, so make them 0 as well
+            if (key0 + 16 > kv || bad) {
+                const int row = ks + (lane & 15);
+                if (key0 + (lane & 15) >= kv || bad) {
+                    uint8_t* vr = stage + (2 + (lane >> 4)) * kHalf + row * 128;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(vr + 16 * c) = make_uint4(0, 0, 0, 0);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the copy that reuses the stage
+                __syncwarp();
+            }
+            float c0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+            float c1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+#pragma unroll
+            for (int w = 1; w < 4; w <<= 1) {
+                c0 = fmaxf(c0, __shfl_xor_sync(0xffffffffu, c0, w));
+                c1 = fmaxf(c1, __shfl_xor_sync(0xffffffffu, c1, w));
+            }
+            c0 *= sl2;
+            c1 *= sl2;
+            float f0 = 1.f, f1 = 1.f;
+            if (m0 == -CUDART_INF_F) m0 = c0;
+            else if (c0 > m0 + kRaise) f0 = ex2f(m0 - c0), m0 = c0;
+            if (m1 == -CUDART_INF_F) m1 = c1;
+            else if (c1 > m1 + kRaise) f1 = ex2f(m1 - c1), m1 = c1;
+            if (__any_sync(0xffffffffu, f0 != 1.f || f1 != 1.f)) {
+                l0 *= f0;
+                l1 *= f1;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    o[k][0] *= f0;
+                    o[k][1] *= f0;
+                    o[k][2] *= f1;
+                    o[k][3] *= f1;
+                }
+            }
+            const float mu0 = m0 == -CUDART_INF_F ? 0.f : m0, mu1 = m1 == -CUDART_INF_F ? 0.f : m1;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                s[j][0] = ex2f(fmaf(s[j][0], sl2, -mu0));
+                s[j][1] = ex2f(fmaf(s[j][1], sl2, -mu0));
+                s[j][2] = ex2f(fmaf(s[j][2], sl2, -mu1));
+                s[j][3] = ex2f(fmaf(s[j][3], sl2, -mu1));
+                l0 += s[j][0] + s[j][1];
+                l1 += s[j][2] + s[j][3];
+            }
+            uint32_t p[4] = {pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]), pack_bf16(s[1][0], s[1][1]),
+                             pack_bf16(s[1][2], s[1][3])};
+            // O += P V: 16 keys, 16 columns a step
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const int ch = 2 * (c & 3) + vc;
+                uint32_t b[4];
+                ldsm4t(b, vb + (c >> 2) * kHalf + vrow * 128 + ((ch ^ (vrow & 7)) << 4));
+                mma16816(o[2 * c], p, b[0], b[1]);
+                mma16816(o[2 * c + 1], p, b[2], b[3]);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[st]);
+        }
+        // ---- join the eight warps: maxima and denominators, then the outputs in two buffers, in a fixed order
+#pragma unroll
+        for (int w = 1; w < 4; w <<= 1) {
+            l0 += __shfl_xor_sync(0xffffffffu, l0, w);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, w);
+        }
+        if (t4 == 0) {
+            jm[warp][g4] = m0;
+            jm[warp][g4 + 8] = m1;
+            jl[warp][g4] = l0;
+            jl[warp][g4 + 8] = l1;
+        }
+        const int row0 = ud.row0, tok0 = ud.tok0, g = ud.g, p0 = ud.c0, p1 = ud.c1, slot0 = ud.slot0;
+        named_sync<32 * kConsumers>(1);
+        if (lane == 0) mbar_arrive(&u_empty[u % kUnits]);
+        float M0 = -CUDART_INF_F, M1 = -CUDART_INF_F;
+#pragma unroll
+        for (int w = 0; w < kConsumers; ++w) {
+            M0 = fmaxf(M0, jm[w][g4]);
+            M1 = fmaxf(M1, jm[w][g4 + 8]);
+        }
+        const float w0 = M0 == -CUDART_INF_F ? 0.f : ex2f(m0 - M0), w1 = M1 == -CUDART_INF_F ? 0.f : ex2f(m1 - M1);
+#pragma unroll 1
+        for (int turn = 0; turn < kConsumers / 2; ++turn) {
+            if ((warp >> 1) == turn) {
+                float* buf = join + (warp & 1) * kMergeF;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    float2* x0 = reinterpret_cast<float2*>(buf + g4 * kMergeStride + 8 * k + 2 * t4);
+                    float2* x1 = reinterpret_cast<float2*>(buf + (g4 + 8) * kMergeStride + 8 * k + 2 * t4);
+                    if (in0) {
+                        float2 v = turn ? *x0 : make_float2(0.f, 0.f);
+                        *x0 = make_float2(fmaf(o[k][0], w0, v.x), fmaf(o[k][1], w0, v.y));
+                    }
+                    if (in1) {
+                        float2 v = turn ? *x1 : make_float2(0.f, 0.f);
+                        *x1 = make_float2(fmaf(o[k][2], w1, v.x), fmaf(o[k][3], w1, v.y));
+                    }
+                }
+            }
+            named_sync<32 * kConsumers>(1);
+        }
+        bf16* out = reinterpret_cast<bf16*>(a.out);
+        auto out_ptr = [&](int r) {
+            return out + (long long)(row0 + tok0 + r / a.G) * a.out_stride + (g * a.G + r % a.G) * kD;
+        };
+        auto row_ml = [&](int r, float& M, float& L) {
+            M = -CUDART_INF_F;
+#pragma unroll
+            for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, jm[w][r]);
+            L = 0.f;
+            if (M != -CUDART_INF_F)
+#pragma unroll
+                for (int w = 0; w < kConsumers; ++w) L = fmaf(jl[w][r], ex2f(jm[w][r] - M), L);
+        };
+        const int tid = threadIdx.x;
+        const size_t mine = (size_t)((int)blockIdx.x == p0 ? slot0 : 2 * blockIdx.x) * kRows;
+        for (int e = tid; e < nrow * 32; e += 32 * kConsumers) {  // a warp per row, four columns per lane
+            const int r = e >> 5, c = (e & 31) * 4;
+            float M, L;
+            row_ml(r, M, L);
+            const float4 x = *reinterpret_cast<const float4*>(join + r * kMergeStride + c);
+            const float4 y = *reinterpret_cast<const float4*>(join + kMergeF + r * kMergeStride + c);
+            float4 v = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+            if (p0 < 0) {
+                const float inv = L > 0.f ? 1.f / L : 0.f;
+                if (alive) store4<bf16>(out_ptr(r) + c, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+            } else {
+                __stcg(reinterpret_cast<float4*>(a.part_o + (mine + r) * kD + c), v);
+                if (lane == 0) __stcg(reinterpret_cast<float2*>(a.part_ml) + mine + r, make_float2(M, L));
+            }
+        }
+        if (p0 >= 0) {
+            __threadfence();
+            named_sync<32 * kConsumers>(1);
+            if (tid == 0)
+                last_s = atomicInc(reinterpret_cast<unsigned*>(a.counters) + p0, (unsigned)(p1 - p0)) == (unsigned)(p1 - p0);
+            named_sync<32 * kConsumers>(1);
+            if (last_s) {
+                __threadfence();
+                auto piece = [&](int c) { return (size_t)(c == p0 ? slot0 : 2 * c) * kRows; };
+                for (int e = tid; e < nrow * 32; e += 32 * kConsumers) {
+                    const int r = e >> 5, c = (e & 31) * 4;
+                    float M = -CUDART_INF_F;
+                    for (int k = p0; k <= p1; ++k) M = fmaxf(M, __ldcg(reinterpret_cast<const float2*>(a.part_ml) + piece(k) + r).x);
+                    float L = 0.f;
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int k = p0; k <= p1 && M != -CUDART_INF_F; ++k) {
+                        const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + piece(k) + r);
+                        const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_o + (piece(k) + r) * kD + c));
+                        const float f = ex2f(ml.x - M);
+                        L = fmaf(ml.y, f, L);
+                        v.x = fmaf(x.x, f, v.x);
+                        v.y = fmaf(x.y, f, v.y);
+                        v.z = fmaf(x.z, f, v.z);
+                        v.w = fmaf(x.w, f, v.w);
+                    }
+                    const float inv = L > 0.f ? 1.f / L : 0.f;
+                    if (alive) store4<bf16>(out_ptr(r) + c, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+                }
+            }
+        }
+        named_sync<32 * kConsumers>(1);  // the join buffers are free for the next unit
+    }
+}
+
+}  // namespace
+
+bool configure_chunk_attention_few() {
+    return cudaFuncSetAttribute(chunk_attn_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem) ==
+               cudaSuccess &&
+           max_shared_carveout((const void*)chunk_attn_few_kernel);
+}
+
+int launch_chunk_attention_few(const ChunkAttnDev& a, int sms, cudaStream_t s) {
+    CUtensorMap pool_map{};
+    const uint64_t rows = (uint64_t)a.n_pages * a.L * 2 * a.Hkv * a.S;
+    // (without pages every key is invalid and the map is never used)
+    if (a.n_pages > 0 && !tc::make_map(&pool_map, a.kv_pool, rows, kD, (uint32_t)a.S)) return -1;
+    const dim3 grid(sms < kChunkCtas ? sms : kChunkCtas), block(kFewThreads);
+    return launched(launch_pdl(chunk_attn_few_kernel, grid, block, kFewSmem, s, 0, pool_map, a));
+}
+
+}  // namespace focus

@@ -345,14 +345,14 @@ template <typename T, int D, int TR> bool configure_one() {
 
 bool configure_chunk_attention_simt() {
     return configure_one<float, 64, 8>() && configure_one<float, 64, 64>() && configure_one<float, 128, 8>() &&
-           configure_one<float, 128, 64>() && configure_one<bf16, 128, 8>() && configure_one<bf16, 128, 64>();
+           configure_one<float, 128, 64>();
 }
 
 template <typename T, int D> int launch_chunk_attention_simt(const ChunkAttnDev& a, int sms, cudaStream_t s) {
     const dim3 grid(2 * sms < kChunkSimtCtas ? 2 * sms : kChunkSimtCtas), block(kThreads);
     int n = 0;
     const long long most = (long long)a.max_new * a.G;
-    if (most > kFew && sizeof(T) == 4) {  // units of 64 query vectors
+    if (most > kFew) {  // units of 64 query vectors
         if (launched(launch_pdl(chunk_attn_simt_kernel<T, D, 64>, grid, block, simt_smem<D, 64>(a.N), s, 0, a)) < 0)
             return -1;
         ++n;
@@ -367,6 +367,5 @@ template <typename T, int D> int launch_chunk_attention_simt(const ChunkAttnDev&
 
 template int launch_chunk_attention_simt<float, 64>(const ChunkAttnDev&, int, cudaStream_t);
 template int launch_chunk_attention_simt<float, 128>(const ChunkAttnDev&, int, cudaStream_t);
-template int launch_chunk_attention_simt<bf16, 128>(const ChunkAttnDev&, int, cudaStream_t);
 
 }  // namespace focus

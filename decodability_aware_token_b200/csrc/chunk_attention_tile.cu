@@ -22,21 +22,15 @@
 // MMAs in flight are waited for (bounded), and TMEM is released.
 #include <math_constants.h>
 
-#include "chunk_work.cuh"
-#include "tc_gemm_kernel.cuh"
+#include "chunk_pipe.cuh"
 
 namespace focus {
 namespace {
 
 using tc::idesc_bf16;
-using tc::mbar_arrive;
-using tc::mbar_expect_tx;
-using tc::mbar_init;
 using tc::smem_desc_sw128;
-using tc::smem_u32;
 using tc::tc_fence_after;
 using tc::tc_fence_before;
-using tc::tma_load_2d;
 using tc::tmem_ld32;
 
 constexpr int kD = 128;
@@ -51,7 +45,6 @@ constexpr int kSoftWarps = 8;                 // 4 per tile: one thread per quer
 constexpr int kTileThreads = 32 * kSoftWarps + 128;  // then one warp for the copies and one per tile for the MMAs
 constexpr int kCopyWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;  // tile t: warp kMmaWarp + t
 constexpr int kFlags = 16;                    // bad-page flags, one per block in flight
-constexpr int kUnits = 4;                     // unit descriptors in flight
 constexpr float kRaise = 8.f;
 constexpr float kExp1 = 0.69328290f, kExp2 = 0.24221095f, kExp3 = 0.05500893f;
 constexpr int kPolyOf8 = 2;                   // of 8 pairs of weights, those computed on the FMA pipe
@@ -210,48 +203,13 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-// The four warps of tile t meet (named barriers 1, 2).
-__device__ __forceinline__ void sync_tile(int t) { asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory"); }
-__device__ __forceinline__ bool tile_agrees(int t, bool ok) {
-    uint32_t all;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
-        "bar.red.and.pred p, %1, 128, q;\n\tselp.b32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(all)
-        : "r"(1 + t), "r"((uint32_t)ok)
-        : "memory");
-    return all != 0;
-}
-
-// As tc::mbar_wait, but the clock is read only every 64 failed tries: the waiting warps share their SM
-// quarter's issue slots with the ones that work.
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, int* err) {
-    const uint32_t addr = smem_u32(bar);
-    if (tc::mbar_try(addr, parity)) return true;
-    const long long t0 = clock64();
-    for (;;) {
-#pragma unroll 1
-        for (int i = 0; i < 64; ++i)
-            if (tc::mbar_try(addr, parity)) return true;
-        if (clock64() - t0 > tc::kWaitCycles) {
-            raise_err(err, FOCUS_DEVERR_TIMEOUT);
-            return false;
-        }
-    }
-}
+// The four warps of tile t meet at named barrier 1 + t.
+__device__ __forceinline__ void sync_tile(int t) { named_sync<128>(1 + t); }
 
 // Registers by role: 384 threads start with 168 each (64512); the softmax warps hold a row's 128 scores, the
 // last warpgroup (copies, MMAs) needs few: 256 x 208 + 128 x 88 = 64512.
 constexpr int kSoftRegs = 208, kIssueRegs = 88;
 static_assert(32 * kSoftWarps * kSoftRegs + 128 * kIssueRegs <= kTileThreads * 168, "register split");
-
-// One piece of a unit, written by the copy thread as it reaches it and read by the other roles.
-struct UnitDesc {
-    int row0, n, kv;          // the request
-    int g, tok0;              // KV head, first token
-    int blk0, nb;             // key blocks of the piece (nb = 0: no more units)
-    int c0, c1, slot0;        // CTAs that hold pieces (c0 = -1: the whole unit is here), scratch slot of c0's
-};
 
 __global__ void __launch_bounds__(kTileThreads, 1)
 chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_constant__ CUtensorMap q_map,
@@ -308,7 +266,7 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
     pdl_wait();
 
     const int tpt = 128 / a.G;  // tokens per tile
-    const ChunkShape sh{2 * tpt, kChunkFewRows, 0x7fffffff};
+    const ChunkShape sh{2 * tpt, a.G <= kChunkFewRows ? kChunkFewRows : 0, 0x7fffffff};
     chunk_schedule<kKeys>(a, sh, min_blocks, reinterpret_cast<long long*>(ring), red, &rg);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the ring held the schedule's sums
     __syncthreads();
@@ -327,22 +285,7 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
             ChunkWalk<kKeys> wk;
             auto publish = [&](bool live) {
                 if (!wait_bar(&u_empty[d % kUnits], ((d / kUnits) & 1u) ^ 1u, a.err)) return false;
-                UnitDesc& ud = unit_s[d % kUnits];
-                ud.nb = 0;
-                if (live) {
-                    ud.row0 = wk.r.row0;
-                    ud.n = wk.r.n;
-                    ud.kv = wk.r.kv;
-                    ud.g = wk.g;
-                    ud.tok0 = wk.k * sh.tok;
-                    ud.blk0 = wk.blk0;
-                    ud.nb = wk.blk1 - wk.blk0;
-                    ud.c0 = -1;
-                    if (!wk.whole()) {
-                        wk.pieces(rg, ud.c0, ud.c1);
-                        ud.slot0 = wk.slot(rg, ud.c0);  // (a later CTA's piece of the unit is its first: slot 2c)
-                    }
-                }
+                describe(unit_s[d % kUnits], wk, rg, sh, live);
                 mbar_arrive(&u_full[d % kUnits]);
                 ++d;
                 return true;
@@ -492,7 +435,7 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
         for (uint32_t u = 0;; ++u) {
             // the tile's warps go on or stop together: a wait that gave up in one of them alone would leave the
             // others at a named barrier
-            if (!tile_agrees(t, unit_wait(u))) break;
+            if (!all_agree<128>(1 + t, unit_wait(u))) break;
             const UnitDesc& ud = unit_s[u % kUnits];
             const int nb = ud.nb;
             if (nb == 0) break;
