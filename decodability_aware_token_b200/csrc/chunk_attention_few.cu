@@ -4,7 +4,7 @@
 //
 // Bound by memory: each cached key and value is read once (64 Hkv d bytes ... per 16-key step 8 KB), so the design
 // is a copy that never stops.  One CTA per SM walks its equal share of the batch's key blocks (chunk_work.cuh);
-// one warp issues the pages of 64-key blocks by TMA into a ring of six 32 KB stages and runs on across unit
+// one warp issues the pages of 64-key blocks by TMA into a ring of four 32 KB stages and runs on across unit
 // ends; eight warps consume, four per block, 16 keys each.  A warp keeps its own running maximum, denominator
 // and 16 x 128 output, so nothing is exchanged while a unit lasts; the eight are joined in shared memory at its
 // end, and pieces of a unit that spans CTAs are joined by the CTA that finishes last, in block order.
@@ -21,16 +21,21 @@ namespace {
 constexpr int kD = 128;
 constexpr int kKeys = 64;
 constexpr int kHalf = kKeys * 128;           // [64 keys][64 columns] bf16
-constexpr int kStage = 4 * kHalf;            // K lo, K hi, V lo, V hi: 32 KB
-constexpr int kStages = 6;
+constexpr int kStage = 4 * kHalf;            // per page: K lo, K hi, V lo, V hi of S rows; 32 KB in all
+constexpr int kStages = 4;
+// The two groups of consumers take alternate blocks, so a stage must always be the same group's: a warp may
+// only wait for a stage's next phase when it has waited for the one before (copies land out of order, and a
+// parity wait two phases ahead succeeds at once).
+static_assert(kStages % 2 == 0, "a stage belongs to one group of consumers");
 constexpr int kRows = kChunkFewRows;
 static_assert(kRows == 16, "one m16 tile");
 constexpr int kConsumers = 8;
 constexpr int kFewThreads = 32 * (kConsumers + 1);
-constexpr int kMergeStride = kD + 4;         // floats per row of the join buffers: rows 4 banks apart
-constexpr int kMergeF = kRows * kMergeStride;
-constexpr int kFewSmem = kStages * kStage + 2 * kMergeF * 4 + 1024;
-static_assert(kFewSmem <= 216 * 1024, "shared memory");
+constexpr int kJoinF = 8 * kD;               // floats of a warp's join buffer: 8 rows
+constexpr int kQRow = kD * 2 + 16;           // bytes of a query row in shared memory: rows 4 banks apart
+constexpr int kQBytes = kRows * kQRow;
+constexpr int kFewSmem = kStages * kStage + kConsumers * kJoinF * 4 + kUnits * kQBytes + 1024;
+static_assert(kFewSmem <= 220 * 1024, "shared memory");
 static_assert(kChunkMaxRequests * 8 <= kStages * kStage, "the schedule's sums fit in the ring");
 constexpr float kRaise = 8.f;
 
@@ -67,7 +72,8 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
     pdl_trigger();
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float* join = reinterpret_cast<float*>(ring + kStages * kStage);  // two [16][kMergeStride] buffers
+    float* join = reinterpret_cast<float*>(ring + kStages * kStage);  // [warp][8 rows][128]
+    uint8_t* q_s = reinterpret_cast<uint8_t*>(join + kConsumers * kJoinF);  // [unit][16 rows][kQRow bytes]
     __shared__ __align__(8) uint64_t full[kStages], empty[kStages], u_full[kUnits], u_empty[kUnits];
     __shared__ UnitDesc unit_s[kUnits];
     __shared__ uint32_t bad_s[kStages];       // 16-key groups of the stage whose page id is invalid
@@ -96,18 +102,29 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
     __syncthreads();
 
     if (warp == kConsumers) {
-        // ---- copies: the whole warp walks; lane i issues page i / 4's K lo, K hi, V lo, V hi copy number i % 4
+        // ---- copies: the whole warp walks, one lane issues
+        const uint32_t el = elect_one();
         const int ppb = kKeys / a.S;  // pages per block
         uint32_t n = 0, d = 0;        // stages filled, units described
         bool ok = true;
         ChunkWalk<kKeys> wk;
+        auto all_ok = [&](bool x) { return __all_sync(0xffffffffu, x) != 0; };
+        // describe the unit and start its query rows on their way
         auto publish = [&](bool live) {
-            bool got = wait_bar(&u_empty[d % kUnits], ((d / kUnits) & 1u) ^ 1u, a.err);
-            got = __all_sync(0xffffffffu, got);
-            if (!got) return false;
+            const uint32_t s = d % kUnits;
+            if (!all_ok(wait_bar(&u_empty[s], ((d / kUnits) & 1u) ^ 1u, a.err))) return false;
+            const int nrow = live ? min(sh.tok, wk.r.n - wk.k * sh.tok) * a.G : 0;
             if (lane == 0) {
-                describe(unit_s[d % kUnits], wk, rg, sh, live);
-                mbar_arrive(&u_full[d % kUnits]);
+                describe(unit_s[s], wk, rg, sh, live);
+                mbar_expect_tx(&u_full[s], (uint32_t)nrow * 256u);
+            }
+            __syncwarp();
+            if (lane < nrow) {
+                const bf16* src = reinterpret_cast<const bf16*>(a.q) +
+                                  (long long)(wk.r.row0 + wk.k * sh.tok + lane / a.G) * a.q_stride + (wk.g * a.G + lane % a.G) * kD;
+                asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                             ::"r"(smem_u32(q_s + s * kQBytes + lane * kQRow)), "l"(src), "n"(kD * 2), "r"(smem_u32(&u_full[s]))
+                             : "memory");
             }
             __syncwarp();
             ++d;
@@ -116,35 +133,35 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
         for (wk.start(a, sh, rg); ok && wk.live(); wk.next(a, sh)) {
             ok = publish(true);
             const int32_t* pt = a.page_table + (size_t)wk.b * a.max_pages;
-            int ahead0 = -1, ahead = 0;  // page ids of table entries ahead0 + lane
-            for (int blk = wk.blk0; ok && blk < wk.blk1; ++blk, ++n) {
-                const int key0 = blk * kKeys, p0 = key0 / a.S;
-                const int np = (max(0, min(kKeys, wk.r.kv - key0)) + a.S - 1) / a.S;
-                if (ahead0 < 0 || p0 + ppb > ahead0 + 32) {
+            int p0 = wk.blk0 * ppb;
+            int ahead0 = p0, ahead = p0 + lane < a.max_pages ? pt[p0 + lane] : -1;  // table entries ahead0 + lane
+            const int pages = (wk.r.kv + a.S - 1) / a.S;
+            for (int blk = wk.blk0; ok && blk < wk.blk1; ++blk, ++n, p0 += ppb) {
+                if (p0 + ppb > ahead0 + 32) {
                     ahead0 = p0;
                     ahead = p0 + lane < a.max_pages ? pt[p0 + lane] : -1;
                 }
-                const int page = __shfl_sync(0xffffffffu, ahead, (p0 - ahead0 + (lane >> 2)) & 31);
-                const bool mine = (lane >> 2) < np;
-                const bool good = mine && page >= 0 && page < a.n_pages;
-                const uint32_t good_m = __ballot_sync(0xffffffffu, good), bad_m = __ballot_sync(0xffffffffu, mine && !good);
-                uint32_t bad = 0;
-                for (int p = 0; p < np; ++p)
-                    if ((bad_m >> (4 * p)) & 1u) bad |= ((1u << (a.S / 16)) - 1u) << (p * (a.S / 16));
                 const uint32_t st = n % kStages;
-                ok = __all_sync(0xffffffffu, wait_bar(&empty[st], ((n / kStages) & 1u) ^ 1u, a.err));
+                uint32_t bad = 0;
+                int good = 0;
+                for (int p = 0; p < ppb && p0 + p < pages; ++p) {
+                    const int page = __shfl_sync(0xffffffffu, ahead, p0 + p - ahead0);
+                    if (page >= 0 && page < a.n_pages) ++good;
+                    else bad |= ((1u << (a.S / 16)) - 1u) << (p * (a.S / 16));
+                }
+                ok = all_ok(wait_bar(&empty[st], ((n / kStages) & 1u) ^ 1u, a.err));
                 if (!ok) break;
-                if (lane == 0) {
+                if (el) {
                     if (bad) raise_err(a.err, FOCUS_DEVERR_PAGE_ID);
                     bad_s[st] = bad;
-                    mbar_expect_tx(&full[st], (uint32_t)__popc(good_m) * (uint32_t)a.S * 128u);
+                    mbar_expect_tx(&full[st], (uint32_t)(good * a.S) * 512u);
                 }
                 __syncwarp();
-                if (good) {
-                    const int kv = (lane >> 1) & 1, h = lane & 1;
-                    const int row = (int)(((((long long)page * a.L + a.layer) * 2 + kv) * a.Hkv + wk.g) * a.S);
-                    tma_load_2d(&pool_map, &full[st], ring + st * kStage + (2 * kv + h) * kHalf + (lane >> 2) * a.S * 128,
-                                h * 64, row);
+                for (int p = 0; p < ppb && p0 + p < pages; ++p) {
+                    const int page = __shfl_sync(0xffffffffu, ahead, p0 + p - ahead0);
+                    if (page >= 0 && page < a.n_pages && el)
+                        tma_load_pool(&pool_map, &full[st], ring + st * kStage + p * a.S * 512, 0, 0,
+                                      (int)(((long long)page * a.L + a.layer) * 2 * a.Hkv) + wk.g);
                 }
                 __syncwarp();
             }
@@ -152,6 +169,7 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
         if (ok) publish(false);
         // never leave with copies in flight
         for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i) wait_bar(&full[i % kStages], (i / kStages) & 1u, a.err);
+        for (uint32_t i = d > kUnits ? d - kUnits : 0; i < d; ++i) wait_bar(&u_full[i % kUnits], (i / kUnits) & 1u, a.err);
         return;
     }
 
@@ -160,8 +178,10 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
     const int g4 = lane >> 2, t4 = lane & 3;          // fragment row, column pair
     const float sl2 = a.scale * 1.4426950408889634f;
     // ldmatrix row addresses within a stage: K (keys x 32 columns a step), V transposed (16 keys x 16 columns)
-    const int krow = ks + (lane & 7), kc = lane >> 3;               // + 8 keys per n tile, 16-byte column kc
-    const int vrow = ks + (lane & 7) + ((lane >> 3) & 1) * 8, vc = lane >> 4;
+    // (the warp's 16 keys lie in one page: S is a multiple of 16)
+    const uint32_t key_off = (uint32_t)(ks / a.S * a.S * 512 + ks % a.S * 128), half_off = (uint32_t)a.S * 128u;
+    const int krow = lane & 7, kc = lane >> 3;                      // + 8 keys per n tile, 16-byte column kc
+    const int vrow = (lane & 7) + ((lane >> 3) & 1) * 8, vc = lane >> 4;
     uint32_t n = 0;
     bool alive = true;
     for (uint32_t u = 0;; ++u) {
@@ -175,16 +195,14 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
         const int pos0 = kv - ud.n + ud.tok0;
         // query fragments: rows g4 and g4 + 8, columns 16 s + 2 t4 (+ 1) and + 8
         uint32_t q[8][4];
-        const bf16* qp = reinterpret_cast<const bf16*>(a.q) + (long long)(ud.row0 + ud.tok0) * a.q_stride + ud.g * a.G * kD;
-        auto q_row = [&](int r) { return qp + (long long)(r / a.G) * a.q_stride + (r % a.G) * kD + 2 * t4; };
         const bool in0 = g4 < nrow, in1 = g4 + 8 < nrow;
-        const bf16 *q0 = q_row(g4), *q1 = q_row(g4 + 8);
+        const uint8_t* qr = q_s + (u % kUnits) * kQBytes + g4 * kQRow + 4 * t4;
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
-            q[s][0] = in0 ? *reinterpret_cast<const uint32_t*>(q0 + 16 * s) : 0u;
-            q[s][1] = in1 ? *reinterpret_cast<const uint32_t*>(q1 + 16 * s) : 0u;
-            q[s][2] = in0 ? *reinterpret_cast<const uint32_t*>(q0 + 16 * s + 8) : 0u;
-            q[s][3] = in1 ? *reinterpret_cast<const uint32_t*>(q1 + 16 * s + 8) : 0u;
+            q[s][0] = in0 ? *reinterpret_cast<const uint32_t*>(qr + 32 * s) : 0u;
+            q[s][1] = in1 ? *reinterpret_cast<const uint32_t*>(qr + 8 * kQRow + 32 * s) : 0u;
+            q[s][2] = in0 ? *reinterpret_cast<const uint32_t*>(qr + 32 * s + 16) : 0u;
+            q[s][3] = in1 ? *reinterpret_cast<const uint32_t*>(qr + 8 * kQRow + 32 * s + 16) : 0u;
         }
         const int lim0 = in0 ? chunk_visible(pos0 + g4 / a.G, kv, a.mask_block) : 0;
         const int lim1 = in1 ? chunk_visible(pos0 + (g4 + 8) / a.G, kv, a.mask_block) : 0;
@@ -204,7 +222,7 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
             const int key0 = (ud.blk0 + i) * kKeys + ks;
             const uint32_t bad = (bad_s[st] >> (ks >> 4)) & 1u;
             uint8_t* stage = ring + st * kStage;
-            const uint32_t kb = smem_u32(stage), vb = kb + 2 * kHalf;
+            const uint32_t kb = smem_u32(stage) + key_off, vb = kb + 2 * half_off;
             float s[2][4];
 #pragma unroll
             for (int j = 0; j < 2; ++j)
@@ -218,7 +236,7 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
                 for (int j = 0; j < 2; ++j) {
                     const int row = krow + 8 * j;
                     uint32_t b[4];
-                    ldsm4(b, kb + (c >> 1) * kHalf + row * 128 + ((ch ^ (row & 7)) << 4));
+                    ldsm4(b, kb + (c >> 1) * half_off + row * 128 + ((ch ^ (row & 7)) << 4));
                     mma16816(s[j], q[2 * c], b[0], b[1]);
                     mma16816(s[j], q[2 * c + 1], b[2], b[3]);
                 }
@@ -234,9 +252,8 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
             }
             // V rows of keys that do not exist may hold anything: their weight is 0, so make them 0 as well
             if (key0 + 16 > kv || bad) {
-                const int row = ks + (lane & 15);
                 if (key0 + (lane & 15) >= kv || bad) {
-                    uint8_t* vr = stage + (2 + (lane >> 4)) * kHalf + row * 128;
+                    uint8_t* vr = stage + key_off + (2 + (lane >> 4)) * half_off + (lane & 15) * 128;
 #pragma unroll
                     for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(vr + 16 * c) = make_uint4(0, 0, 0, 0);
                 }
@@ -285,14 +302,14 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
             for (int c = 0; c < 8; ++c) {
                 const int ch = 2 * (c & 3) + vc;
                 uint32_t b[4];
-                ldsm4t(b, vb + (c >> 2) * kHalf + vrow * 128 + ((ch ^ (vrow & 7)) << 4));
+                ldsm4t(b, vb + (c >> 2) * half_off + vrow * 128 + ((ch ^ (vrow & 7)) << 4));
                 mma16816(o[2 * c], p, b[0], b[1]);
                 mma16816(o[2 * c + 1], p, b[2], b[3]);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[st]);
         }
-        // ---- join the eight warps: maxima and denominators, then the outputs in two buffers, in a fixed order
+        // ---- join the eight warps: maxima and denominators, then the outputs, eight rows at a time, in warp order
 #pragma unroll
         for (int w = 1; w < 4; w <<= 1) {
             l0 += __shfl_xor_sync(0xffffffffu, l0, w);
@@ -305,63 +322,49 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
             jl[warp][g4 + 8] = l1;
         }
         const int row0 = ud.row0, tok0 = ud.tok0, g = ud.g, p0 = ud.c0, p1 = ud.c1, slot0 = ud.slot0;
-        named_sync<32 * kConsumers>(1);
-        if (lane == 0) mbar_arrive(&u_empty[u % kUnits]);
-        float M0 = -CUDART_INF_F, M1 = -CUDART_INF_F;
-#pragma unroll
-        for (int w = 0; w < kConsumers; ++w) {
-            M0 = fmaxf(M0, jm[w][g4]);
-            M1 = fmaxf(M1, jm[w][g4 + 8]);
-        }
-        const float w0 = M0 == -CUDART_INF_F ? 0.f : ex2f(m0 - M0), w1 = M1 == -CUDART_INF_F ? 0.f : ex2f(m1 - M1);
-#pragma unroll 1
-        for (int turn = 0; turn < kConsumers / 2; ++turn) {
-            if ((warp >> 1) == turn) {
-                float* buf = join + (warp & 1) * kMergeF;
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    float2* x0 = reinterpret_cast<float2*>(buf + g4 * kMergeStride + 8 * k + 2 * t4);
-                    float2* x1 = reinterpret_cast<float2*>(buf + (g4 + 8) * kMergeStride + 8 * k + 2 * t4);
-                    if (in0) {
-                        float2 v = turn ? *x0 : make_float2(0.f, 0.f);
-                        *x0 = make_float2(fmaf(o[k][0], w0, v.x), fmaf(o[k][1], w0, v.y));
-                    }
-                    if (in1) {
-                        float2 v = turn ? *x1 : make_float2(0.f, 0.f);
-                        *x1 = make_float2(fmaf(o[k][2], w1, v.x), fmaf(o[k][3], w1, v.y));
-                    }
-                }
-            }
-            named_sync<32 * kConsumers>(1);
-        }
         bf16* out = reinterpret_cast<bf16*>(a.out);
         auto out_ptr = [&](int r) {
             return out + (long long)(row0 + tok0 + r / a.G) * a.out_stride + (g * a.G + r % a.G) * kD;
         };
-        auto row_ml = [&](int r, float& M, float& L) {
-            M = -CUDART_INF_F;
-#pragma unroll
-            for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, jm[w][r]);
-            L = 0.f;
-            if (M != -CUDART_INF_F)
-#pragma unroll
-                for (int w = 0; w < kConsumers; ++w) L = fmaf(jl[w][r], ex2f(jm[w][r] - M), L);
-        };
         const int tid = threadIdx.x;
         const size_t mine = (size_t)((int)blockIdx.x == p0 ? slot0 : 2 * blockIdx.x) * kRows;
-        for (int e = tid; e < nrow * 32; e += 32 * kConsumers) {  // a warp per row, four columns per lane
-            const int r = e >> 5, c = (e & 31) * 4;
-            float M, L;
-            row_ml(r, M, L);
-            const float4 x = *reinterpret_cast<const float4*>(join + r * kMergeStride + c);
-            const float4 y = *reinterpret_cast<const float4*>(join + kMergeF + r * kMergeStride + c);
-            float4 v = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
-            if (p0 < 0) {
-                const float inv = L > 0.f ? 1.f / L : 0.f;
-                if (alive) store4<bf16>(out_ptr(r) + c, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-            } else {
-                __stcg(reinterpret_cast<float4*>(a.part_o + (mine + r) * kD + c), v);
-                if (lane == 0) __stcg(reinterpret_cast<float2*>(a.part_ml) + mine + r, make_float2(M, L));
+#pragma unroll 1
+        for (int half = 0; half < 2 && 8 * half < nrow; ++half) {
+            if (half) named_sync<32 * kConsumers>(1);  // the first eight rows have been read
+            if (half ? in1 : in0) {
+                // odd rows swap their float2 pairs, so that two rows' stores do not meet on the same banks
+                float* buf = join + warp * kJoinF + g4 * kD + 2 * (t4 ^ ((g4 & 1) << 1));
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    *reinterpret_cast<float2*>(buf + 8 * k) = half ? make_float2(o[k][2], o[k][3]) : make_float2(o[k][0], o[k][1]);
+            }
+            named_sync<32 * kConsumers>(1);
+            if (half == 0 && lane == 0) mbar_arrive(&u_empty[u % kUnits]);
+            const int r = 8 * half + warp;  // a warp per row, four columns per lane
+            if (r < nrow) {
+                const int c = lane * 4;
+                float M = -CUDART_INF_F, L = 0.f;
+#pragma unroll
+                for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, jm[w][r]);
+                const float mu = M == -CUDART_INF_F ? 0.f : M;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < kConsumers; ++w) {
+                    const float f = ex2f(jm[w][r] - mu);
+                    const float4 x = *reinterpret_cast<const float4*>(join + w * kJoinF + warp * kD + (c ^ ((warp & 1) << 2)));
+                    L = fmaf(jl[w][r], f, L);
+                    v.x = fmaf(x.x, f, v.x);
+                    v.y = fmaf(x.y, f, v.y);
+                    v.z = fmaf(x.z, f, v.z);
+                    v.w = fmaf(x.w, f, v.w);
+                }
+                if (p0 < 0) {
+                    const float inv = L > 0.f ? 1.f / L : 0.f;
+                    if (alive) store4<bf16>(out_ptr(r) + c, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+                } else {
+                    __stcg(reinterpret_cast<float4*>(a.part_o + (mine + r) * kD + c), v);
+                    if (lane == 0) __stcg(reinterpret_cast<float2*>(a.part_ml) + mine + r, make_float2(M, L));
+                }
             }
         }
         if (p0 >= 0) {
@@ -407,10 +410,8 @@ bool configure_chunk_attention_few() {
 }
 
 int launch_chunk_attention_few(const ChunkAttnDev& a, int sms, cudaStream_t s) {
-    CUtensorMap pool_map{};
-    const uint64_t rows = (uint64_t)a.n_pages * a.L * 2 * a.Hkv * a.S;
-    // (without pages every key is invalid and the map is never used)
-    if (a.n_pages > 0 && !tc::make_map(&pool_map, a.kv_pool, rows, kD, (uint32_t)a.S)) return -1;
+    CUtensorMap pool_map{};  // (without pages every key is invalid and the map is never used)
+    if (a.n_pages > 0 && !make_pool_map(&pool_map, a, 2, 2)) return -1;
     const dim3 grid(sms < kChunkCtas ? sms : kChunkCtas), block(kFewThreads);
     return launched(launch_pdl(chunk_attn_few_kernel, grid, block, kFewSmem, s, 0, pool_map, a));
 }

@@ -289,9 +289,10 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_attn_simt_kernel(ChunkAttnD
             continue;
         }
         // ---- a shared unit: leave the piece in scratch; the last CTA to arrive adds the pieces in order
-        int c0, c1;
-        wk.pieces(rg, c0, c1);
-        const size_t mine = (size_t)wk.slot(rg, blockIdx.x);
+        int c0, c1, slot0;
+        wk.pieces(rg, c0, c1, slot0);
+        auto piece = [&](int c) { return (size_t)(c == c0 ? slot0 : 2 * c); };
+        const size_t mine = piece(blockIdx.x);
         for (int i = tid; i < nrow * (D / 4); i += kThreads) {
             const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
             __stcg(reinterpret_cast<float4*>(a.part_o + (mine * TR + r) * D + c),
@@ -308,12 +309,12 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_attn_simt_kernel(ChunkAttnD
             const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
             float m = -CUDART_INF_F;
             for (int p = c0; p <= c1; ++p)
-                m = fmaxf(m, __ldcg(reinterpret_cast<const float2*>(a.part_ml) + (size_t)wk.slot(rg, p) * TR + r).x);
+                m = fmaxf(m, __ldcg(reinterpret_cast<const float2*>(a.part_ml) + piece(p) * TR + r).x);
             const float mu = m == -CUDART_INF_F ? 0.f : m;
             float l = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int p = c0; p <= c1; ++p) {
-                const size_t at = (size_t)wk.slot(rg, p) * TR + r;
+                const size_t at = piece(p) * TR + r;
                 const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + at);
                 const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D + c));
                 const float f = exp2f(ml.x - mu);

@@ -61,11 +61,6 @@ __device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* ba
 // The MMA warp runs its loop with all lanes and one elected lane issues: loop counters and descriptors stay
 // uniform, which the issue needs (a loop inside `if (lane == 0)` issued one MMA per 85 cycles, slower than
 // the 64 that one takes).
-__device__ __forceinline__ uint32_t elect_one() {
-    uint32_t e;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}\n" : "=r"(e));
-    return e;
-}
 __device__ __forceinline__ void mma_ss(uint32_t elected, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
                                        uint32_t acc) {
     asm volatile(
@@ -333,9 +328,11 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
 #pragma unroll
                         for (int p = 0; p < kKeys / 16; ++p) {
                             if (p < np && page[p] >= 0) {
-                                const int row = (int)(((((long long)page[p] * a.L + a.layer) * 2 + kv) * a.Hkv + wk.g) * a.S);
-                                tma_load_2d(&pool_map, &kv_full[st], dst + p * a.S * 128, 0, row);
-                                tma_load_2d(&pool_map, &kv_full[st], dst + kHalf + p * a.S * 128, 64, row);
+                                const int x = (int)(((long long)page[p] * a.L + a.layer) * 2 * a.Hkv) + wk.g;
+                                // (the map's box holds both column halves when a page is a whole block)
+                                tma_load_pool(&pool_map, &kv_full[st], dst + p * a.S * 128, 0, kv, x);
+                                if (a.S < kKeys)
+                                    tma_load_pool(&pool_map, &kv_full[st], dst + kHalf + p * a.S * 128, 1, kv, x);
                             }
                         }
                     }
@@ -378,7 +375,11 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
                 __syncwarp();
                 if (el) mbar_arrive(&u_empty[u % kUnits]);
                 if (nb == 0) break;
-                if (!mine) {  // a short unit's second tile: give its ring slots back as they come
+                if (!mine) {
+                    // a short unit's second tile: give the queries and the ring slots back as they come (waiting for
+                    // each, since a parity wait must not be two phases ahead)
+                    if (!wait_bar(&q_full, u & 1u, a.err)) break;
+                    __syncwarp();
                     if (el) mbar_arrive(&q_empty);
                     for (int j = 0; ok && j < 2 * nb; ++j, ++n) {
                         ok = full(n);
@@ -658,9 +659,8 @@ bool configure_chunk_attention_tile() {
 int launch_chunk_attention_tile(const ChunkAttnDev& a, int sms, cudaStream_t s) {
     CUtensorMap q_map, pool_map;
     if (!make_q_map(&q_map, a)) return -1;
-    const uint64_t rows = (uint64_t)a.n_pages * a.L * 2 * a.Hkv * a.S;
     if (a.n_pages > 0) {
-        if (!tc::make_map(&pool_map, a.kv_pool, rows, kD, (uint32_t)a.S)) return -1;
+        if (!make_pool_map(&pool_map, a, a.S == kKeys ? 2 : 1, 1)) return -1;
     } else {
         pool_map = q_map;  // never used: without pages every key is invalid
     }

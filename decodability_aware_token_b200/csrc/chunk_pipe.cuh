@@ -11,7 +11,6 @@ using tc::mbar_arrive;
 using tc::mbar_expect_tx;
 using tc::mbar_init;
 using tc::smem_u32;
-using tc::tma_load_2d;
 
 constexpr int kUnits = 4;  // unit descriptors in flight
 
@@ -66,10 +65,37 @@ __device__ __forceinline__ void describe(UnitDesc& ud, const ChunkWalk<KEYS>& wk
     ud.blk0 = wk.blk0;
     ud.nb = wk.blk1 - wk.blk0;
     ud.c0 = -1;
-    if (!wk.whole()) {
-        wk.pieces(rg, ud.c0, ud.c1);
-        ud.slot0 = wk.slot(rg, ud.c0);  // (a later CTA's piece of the unit is its first: slot 2c)
-    }
+    if (!wk.whole()) wk.pieces(rg, ud.c0, ud.c1, ud.slot0);
+}
+
+// The pool's rows of 128 columns for TMA, as (64 columns, S tokens, column half, K / V, x) with
+// x = (page L + layer) 2 Hkv + head: one copy takes a page's K or V of a head, or both, as `halves` x `kvs`
+// tiles of [S][64 columns] with 128-byte rows, swizzled.  A copy instruction costs its issuing thread some
+// 200 cycles whatever it moves, so the fewest and largest are used.
+inline bool make_pool_map(CUtensorMap* m, const ChunkAttnDev& a, int halves, int kvs) {
+    auto fn = tc::encode_fn();
+    if (!fn) return false;
+    const cuuint64_t row = 256, head = (cuuint64_t)a.S * row;
+    const cuuint64_t dims[5] = {64, (cuuint64_t)a.S, 2, 2, (cuuint64_t)a.n_pages * a.L * 2 * a.Hkv};
+    const cuuint64_t strides[4] = {row, 128, head * a.Hkv, head};
+    const cuuint32_t box[5] = {64, (cuuint32_t)a.S, (cuuint32_t)halves, (cuuint32_t)kvs, 1};
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(a.kv_pool), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+__device__ __forceinline__ void tma_load_pool(const CUtensorMap* map, uint64_t* bar, void* dst, int half, int kv, int x) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %3, %4, %5, %6}], [%2];"
+        ::"r"(smem_u32(dst)), "l"(map), "r"(smem_u32(bar)), "r"(0), "r"(half), "r"(kv), "r"(x)
+        : "memory");
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}\n" : "=r"(e));
+    return e;
 }
 
 }  // namespace

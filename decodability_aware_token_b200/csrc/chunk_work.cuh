@@ -2,9 +2,9 @@
 //
 // A unit is (request b, KV head g, tile k of `tok` tokens); it walks ceil(visible keys / KEYS) key blocks
 // (at least one, so that rows that see nothing are still written).  The units of a launch, in the order
-// b, g, k, form one line of W blocks, and CTA c of C takes blocks [W c / C, W (c + 1) / C): every CTA walks
-// the same number of key blocks whatever the lengths are, and at most its first and its last unit are
-// shared with neighbours.  Shared units write unnormalised partial results; the CTA that arrives last adds
+// b, g, k, form one line of W blocks, and CTA c of C takes an equal share of it (W / C blocks, the first W % C
+// CTAs one more): every CTA walks the same number of key blocks whatever the lengths are, and at most its
+// first and its last unit are shared with neighbours.  Shared units write unnormalised partial results; the CTA that arrives last adds
 // them in block order, so the result does not depend on the order of arrival.
 //
 // Each CTA finds its own range from the lengths alone (a scan over the requests in shared memory, about a
@@ -38,7 +38,8 @@ __device__ __forceinline__ ChunkReq chunk_req(const ChunkAttnDev& a, int b, bool
 
 // Keys visible at position pos (the API clamps mask_block so that nothing overflows).
 __device__ __forceinline__ int chunk_visible(int pos, int kv, int mask_block) {
-    return pos < 0 ? 0 : min(kv, (pos / mask_block + 1) * mask_block);
+    if (pos < 0) return 0;
+    return min(kv, mask_block == 1 ? pos + 1 : (pos / mask_block + 1) * mask_block);
 }
 
 // Key blocks of tile k
@@ -58,19 +59,27 @@ __device__ __forceinline__ int chunk_tiles(const ChunkAttnDev& a, const ChunkSha
     return v > sh.lo && v <= sh.hi ? (r.n + sh.tok - 1) / sh.tok : 0;
 }
 
-struct ChunkRange {
-    long long W, w0, w1;  // all blocks, this CTA's range (w0 == w1: none)
-    int C;                // CTAs that share the line
-    int b, g, k, blk;     // where w0 lies
-};
-
-// CTA whose range holds block w: the largest c with floor(W c / C) <= w.
-__device__ __forceinline__ int chunk_owner(long long w, long long W, int C) {
-    return (int)(((w + 1) * C - 1) / W);
+// 64-bit quotient, in 32 bits where both fit (five times as fast)
+__device__ __forceinline__ long long chunk_div(long long x, long long y) {
+    return ((unsigned long long)(x | y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
 }
 
-// Fill *out (shared memory) for this CTA.  `scr` holds N + 1 long longs of shared memory, `red` 32.  Every
-// thread of the block calls it; it ends with a barrier.  min_blocks: smallest useful share of a CTA.
+struct ChunkRange {
+    long long w0, w1;     // this CTA's blocks of the line (w0 == w1: none)
+    long long share;      // W / C
+    int extra;            // W % C: CTAs 0 .. extra - 1 have share + 1 blocks
+    int b, g, k, blk;     // where w0 lies
+
+    __device__ __forceinline__ long long start(int c) const { return share * c + min(c, extra); }
+    // CTA whose range holds block w
+    __device__ __forceinline__ int owner(long long w) const {
+        const long long big = (share + 1) * extra;
+        return w < big ? (int)chunk_div(w, share + 1) : extra + (int)chunk_div(w - big, share);
+    }
+};
+
+// Fill *out (shared memory) for this CTA.  `scr` holds N long longs of shared memory, `red` 32.  Every thread of
+// the block calls it; it ends with a barrier.  min_blocks: smallest useful share of a CTA.
 template <int KEYS>
 __device__ void chunk_schedule(const ChunkAttnDev& a, const ChunkShape& sh, int min_blocks, long long* scr,
                                long long* red, ChunkRange* out) {
@@ -118,38 +127,48 @@ __device__ void chunk_schedule(const ChunkAttnDev& a, const ChunkShape& sh, int 
         __syncthreads();
         long long before = carry, all = 0;
         for (int w = 0; w < nw; ++w) {
-            if (w < warp) before += red[w];
-            all += red[w];
+            const long long x = red[w];
+            if (w < warp) before += x;
+            all += x;
         }
         if (b < a.N) scr[b] = before + v;
         carry += all;
         __syncthreads();
     }
     const long long W = carry;
-    const long long want = (W + min_blocks - 1) / min_blocks;
-    const int C = (int)(want < gridDim.x ? want : (long long)gridDim.x);
     const int c = blockIdx.x;
-    const long long w0 = C > 0 && c < C ? W * c / C : 0, w1 = C > 0 && c < C ? W * (c + 1) / C : 0;
-    if (tid == 0) {
-        out->W = W;
-        out->C = C;
-        out->w0 = w0;
-        out->w1 = w1;
-        out->b = out->g = out->k = out->blk = 0;
+    ChunkRange rg{};
+    if (W > 0) {
+        const long long want = chunk_div(W + min_blocks - 1, min_blocks);
+        const int C = (int)(want < gridDim.x ? want : (long long)gridDim.x);
+        rg.share = chunk_div(W, C);
+        rg.extra = (int)(W - rg.share * C);
+        if (c < C) {
+            rg.w0 = rg.start(c);
+            rg.w1 = rg.start(c + 1);
+        }
     }
+    if (tid == 0) *out = rg;
     __syncthreads();
-    if (w0 < w1) {
-        for (int b = tid; b < a.N; b += nt)
-            if (scr[b] > w0 && (b == 0 || scr[b - 1] <= w0)) out->b = b;
-        __syncthreads();
-        if (warp == 0) {
-            const int b = out->b;
-            const long long base = b ? scr[b - 1] : 0;
-            const long long per = (scr[b] - base) / a.Hkv;  // blocks of one KV head
-            const int g = (int)((w0 - base) / per);
-            long long rem = w0 - base - (long long)g * per;
+    if (rg.w0 < rg.w1) {  // (the same in every thread)
+        int many = 0;
+        for (int b = tid; b < a.N; b += nt) {
+            const long long hi = scr[b], lo = b ? scr[b - 1] : 0;
+            if (hi <= rg.w0 || lo > rg.w0) continue;
+            const long long per = chunk_div(hi - lo, a.Hkv), off = rg.w0 - lo;  // blocks of one KV head
+            const int g = (int)chunk_div(off, per);
+            out->b = b;
+            out->g = g;
+            out->k = 0;
+            out->blk = (int)(off - g * per);  // (more than an int holds only with many tiles, found below)
+            if (chunk_tiles(a, sh, chunk_req(a, b, false)) > 1) many = 1;
+        }
+        if (__syncthreads_or(many) && warp == 0) {
+            const int b = out->b, g = out->g;
             const ChunkReq r = chunk_req(a, b, false);
             const int tiles = chunk_tiles(a, sh, r);
+            const long long lo = b ? scr[b - 1] : 0;
+            long long rem = rg.w0 - lo - g * chunk_div(scr[b] - lo, a.Hkv);
             for (int k0 = 0; k0 < tiles; k0 += 32) {
                 const int k = k0 + lane;
                 const long long mine = k < tiles ? chunk_tile_blocks<KEYS>(r, a.mask_block, sh.tok, k) : 0;
@@ -161,7 +180,6 @@ __device__ void chunk_schedule(const ChunkAttnDev& a, const ChunkShape& sh, int 
                 }
                 const bool here = v > rem && v - mine <= rem;
                 if (here) {
-                    out->g = g;
                     out->k = k;
                     out->blk = (int)(rem - (v - mine));
                 }
@@ -223,16 +241,13 @@ struct ChunkWalk {
         fit(a, sh);
     }
     __device__ __forceinline__ bool whole() const { return blk0 == 0 && blk1 == nblk; }
-    // the CTAs that hold the unit's pieces, and this CTA's slot for its piece
-    __device__ __forceinline__ void pieces(const ChunkRange& rg, int& c0, int& c1) const {
+    // the CTAs that hold the unit's pieces, and the scratch slot of c0's: its first (2 c0) unless the unit
+    // starts inside its range; a later CTA's piece of the unit is its first
+    __device__ __forceinline__ void pieces(const ChunkRange& rg, int& c0, int& c1, int& slot0) const {
         const long long u0 = w - blk0;
-        c0 = chunk_owner(u0, rg.W, rg.C);
-        c1 = chunk_owner(u0 + nblk - 1, rg.W, rg.C);
-    }
-    // slot of CTA c's piece of this unit: its first piece unless the unit starts inside its range
-    __device__ __forceinline__ int slot(const ChunkRange& rg, int c) const {
-        const long long u0 = w - blk0;
-        return 2 * c + (rg.W * c / rg.C < u0 ? 1 : 0);
+        c0 = rg.owner(u0);
+        c1 = rg.owner(u0 + nblk - 1);
+        slot0 = 2 * c0 + (rg.start(c0) < u0 ? 1 : 0);
     }
 };
 
