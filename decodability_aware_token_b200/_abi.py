@@ -1,6 +1,7 @@
 """ctypes mirror of include/focus.h (argument marshalling only)."""
 import ctypes as C
 import os
+import struct
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfocus.so")
 
@@ -103,7 +104,29 @@ class ChunkAttnArgs(C.Structure):
                 ("row_offsets", C.c_void_p), ("kv_len", C.c_void_p), ("page_table", C.c_void_p), ("out", C.c_void_p)]
 
 
+# The same three argument structs as packed bytes (native alignment): a call builds one bytes object instead of
+# setting a field at a time, which costs more host time than a small kernel takes.
+PLAN_PACK = struct.Struct("@5i11P")
+QK_PACK = struct.Struct("@4if4q9P")
+ATTN_PACK = struct.Struct("@7if2q6P")
+
 _lib = None
+_enqueue = None
+
+
+def load_enqueue():
+    """(plan, qk, attention) of the chunk operators, called with a context, packed arguments and a stream.
+    They only check and enqueue, so they keep the GIL: releasing it costs more than it gives here."""
+    global _enqueue
+    if _enqueue is None:
+        load()
+        lib = C.PyDLL(LIB_PATH)
+        fns = (lib.focus_chunk_plan_rows, lib.focus_chunk_qk_norm_rope, lib.focus_chunk_attention)
+        for fn in fns:
+            fn.argtypes = [C.c_void_p, C.c_char_p, C.c_void_p]
+            fn.restype = C.c_int
+        _enqueue = fns
+    return _enqueue
 
 
 def load():

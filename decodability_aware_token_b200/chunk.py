@@ -18,6 +18,11 @@ from . import _abi, _check, _need
 __all__ = ["ChunkContext", "ChunkPlan"]
 
 
+_I32 = torch.int32
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
 @dataclasses.dataclass
 class ChunkPlan:
     """Where a chunk's tokens go: request b owns rows row_offsets[b] .. row_offsets[b + 1] - 1."""
@@ -46,8 +51,11 @@ class ChunkContext:
         if dev.type != "cuda":
             raise ValueError(f"device {dev}: a CUDA device is needed")
         self._lib = _abi.load()
+        self._enqueue = _abi.load_enqueue()
         self.device = torch.device("cuda", torch.cuda.current_device() if dev.index is None else dev.index)
         self.dtype = dtype
+        self._index = self.device.index
+        self._elt = 2 if dtype == torch.bfloat16 else 4
         self.cfg = _abi.ChunkCfg(n_layers, n_q_heads, n_kv_heads, head_dim,
                                  _abi.FOCUS_DTYPE_BF16 if dtype == torch.bfloat16 else _abi.FOCUS_DTYPE_F32, rope_theta)
         self.limits = _abi.ChunkLimits(max_requests, max_pages_per_req)
@@ -65,52 +73,68 @@ class ChunkContext:
                          torch.zeros(max_rows, **kw), torch.zeros(max_rows, **kw), torch.zeros(1, **kw))
 
     # ---- checks -----------------------------------------------------------------------------------------
+    # The fast tests below decide; _need and _heads_error only word the refusal.
     def _ints(self, t, name, shape):
-        _need(t, name, torch.int32, self.device, shape)
+        if not (isinstance(t, torch.Tensor) and t.dtype is _I32 and t.get_device() == self._index and
+                t.shape == shape and t.is_contiguous()):
+            _need(t, name, _I32, self.device, shape)
         return t.data_ptr()
 
-    def _heads(self, t, name, heads):
+    def _heads(self, t, name, rows, heads):
         """[rows, heads, d] with dense heads; returns (data pointer, row stride in elements)."""
+        d = self.head_dim
+        if not (isinstance(t, torch.Tensor) and t.dtype is self.dtype and t.get_device() == self._index and
+                t.shape == (rows, heads, d)):
+            self._heads_error(t, name, rows, heads)
+        s0, s1, s2 = t.stride()
+        if rows <= 1:
+            s0 = heads * d  # the stride of a single row means nothing
+        p = t.data_ptr()
+        if s2 != 1 or (s1 != d and heads > 1):
+            raise ValueError(f"{name}: the heads of a row must be dense")
+        if s0 < heads * d:
+            raise ValueError(f"{name}: rows overlap (stride {s0})")
+        if p % 16 or s0 * self._elt % 16:
+            raise ValueError(f"{name}: rows must be 16-byte aligned")
+        return p, s0
+
+    def _heads_error(self, t, name, rows, heads):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name}: expected a torch.Tensor")
         if t.dtype != self.dtype:
             raise TypeError(f"{name}: dtype {t.dtype}, expected {self.dtype}")
         if t.device != self.device:
             raise ValueError(f"{name}: on {t.device}, expected {self.device}")
-        d = self.head_dim
-        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [rows, {heads}, {d}]")
-        s0, s1, s2 = t.stride()
-        if s2 != 1 or (s1 != d and heads > 1):
-            raise ValueError(f"{name}: the heads of a row must be dense")
-        if t.shape[0] <= 1:
-            s0 = heads * d  # the stride of a single row means nothing
-        if s0 < heads * d:
-            raise ValueError(f"{name}: rows overlap (stride {s0})")
-        if t.data_ptr() % 16 or s0 * t.element_size() % 16:
-            raise ValueError(f"{name}: rows must be 16-byte aligned")
-        return t.data_ptr(), s0
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected ({rows}, {heads}, {self.head_dim})")
 
     def _pool(self, pool, layer):
-        _need(pool, "kv_pool", self.dtype, self.device)
-        s = pool.shape
-        if pool.dim() != 6 or s[1] != self.cfg.n_layers or s[2] != 2 or s[3] != self.n_kv_heads or s[5] != self.head_dim:
-            raise ValueError(f"kv_pool: shape {tuple(s)}, expected [pages, {self.cfg.n_layers}, 2, {self.n_kv_heads}, S, "
-                             f"{self.head_dim}]")
-        if not 0 <= layer < self.cfg.n_layers:
-            raise ValueError(f"layer {layer}: the pool has {self.cfg.n_layers}")
-        return s[0], s[4], pool.data_ptr()
+        if not (isinstance(pool, torch.Tensor) and pool.dtype is self.dtype and pool.get_device() == self._index and
+                pool.is_contiguous()):
+            _need(pool, "kv_pool", self.dtype, self.device)
+        s, L = pool.shape, self.cfg.n_layers
+        if len(s) != 6 or s[1:4] != (L, 2, self.n_kv_heads) or s[5] != self.head_dim:
+            raise ValueError(f"kv_pool: shape {tuple(s)}, expected [pages, {L}, 2, {self.n_kv_heads}, S, {self.head_dim}]")
+        if not 0 <= layer < L:
+            raise ValueError(f"layer {layer}: the pool has {L}")
+        p = pool.data_ptr()
+        if p % 16:
+            raise ValueError("kv_pool: must be 16-byte aligned")
+        return s[0], s[4], p
 
-    def _call(self, fn, args, where, stream):
-        if self._ctx.value is None:
+    def _call(self, which, args, where, stream):
+        if not self._ctx.value:
             raise ValueError(f"{where}: the context is closed")
-        if torch.cuda.current_device() == self.device.index:
-            s = stream.cuda_stream if stream is not None else torch.cuda.current_stream().cuda_stream
-            _check(fn(self._ctx, C.byref(args), s), where)
+        fn = self._enqueue[which]
+        if stream is not None and stream.device_index != self._index:
+            raise ValueError(f"{where}: the stream is on cuda:{stream.device_index}, the context on {self.device}")
+        s = _raw_stream(self._index) if stream is None else stream.cuda_stream
+        if _current_device() == self._index:
+            rc = fn(self._ctx, args, s)
         else:
             with torch.cuda.device(self.device):
-                s = stream.cuda_stream if stream is not None else torch.cuda.current_stream().cuda_stream
-                _check(fn(self._ctx, C.byref(args), s), where)
+                rc = fn(self._ctx, args, s)
+        if rc:
+            _check(rc, where)
 
     # ---- operators --------------------------------------------------------------------------------------
     def plan(self, prefix_len, new_len, page_table, free_pages, free_head, *, page_size: int, n_pages: int,
@@ -121,23 +145,22 @@ class ChunkContext:
         prefix_len, new_len [N] int32; page_table [N, max_pages_per_req] int32, new pages are written into it;
         free_pages [F] int32, taken from index free_head [1] int32 on.  `max_rows` (or the size of `out`)
         bounds the rows.  A request that does not fit gets no rows: row_offsets tells."""
-        n = int(prefix_len.shape[0])
+        n = prefix_len.shape[0]
         if out is None:
             if max_rows is None:
                 raise ValueError("plan: give max_rows or out")
             out = self.alloc_plan(n, max_rows)
-        rows = int(out.row_req.shape[0])
+        rows = out.row_req.shape[0]
         if max_rows is not None and max_rows != rows:
             raise ValueError(f"plan: out holds {rows} rows, max_rows is {max_rows}")
-        i = self._ints
-        args = _abi.ChunkPlanArgs(
-            n, rows, page_size, n_pages, int(free_pages.shape[0]), i(prefix_len, "prefix_len", (n,)),
-            i(new_len, "new_len", (n,)), i(page_table, "page_table", (n, self.limits.max_pages_per_req)),
-            i(free_pages, "free_pages", (int(free_pages.shape[0]),)), i(free_head, "free_head", (1,)),
-            i(out.row_offsets, "row_offsets", (n + 1,)), i(out.kv_len, "kv_len", (n,)), i(out.row_req, "row_req", (rows,)),
-            i(out.row_pos, "row_pos", (rows,)), i(out.row_slot, "row_slot", (rows,)),
+        i, per_req, per_row, n_free = self._ints, (n,), (rows,), free_pages.shape[0]
+        args = _abi.PLAN_PACK.pack(
+            n, rows, page_size, n_pages, n_free, i(prefix_len, "prefix_len", per_req), i(new_len, "new_len", per_req),
+            i(page_table, "page_table", (n, self.limits.max_pages_per_req)), i(free_pages, "free_pages", (n_free,)),
+            i(free_head, "free_head", (1,)), i(out.row_offsets, "row_offsets", (n + 1,)), i(out.kv_len, "kv_len", per_req),
+            i(out.row_req, "row_req", per_row), i(out.row_pos, "row_pos", per_row), i(out.row_slot, "row_slot", per_row),
             i(out.free_next, "free_next", (1,)))
-        self._call(self._lib.focus_chunk_plan_rows, args, "focus_chunk_plan_rows", stream)
+        self._call(0, args, "focus_chunk_plan_rows", stream)
         return out
 
     def qk_norm_rope(self, q, k, v, kv_pool, layer: int, row_pos, row_slot, *, q_norm=None, k_norm=None,
@@ -146,29 +169,29 @@ class ChunkContext:
         """Norm (with the gains given), rotate, store K and V at row_slot; returns the queries
         (focus_chunk_qk_norm_rope).  q [rows, Hq, d], k and v [rows, Hkv, d] may be views of one fused
         projection; rows with row_pos < 0 are skipped."""
-        rows = int(q.shape[0])
-        qp, qs = self._heads(q, "q", self.n_q_heads)
-        kp, ks = self._heads(k, "k", self.n_kv_heads)
-        vp, vs = self._heads(v, "v", self.n_kv_heads)
-        if k.shape[0] != rows or v.shape[0] != rows:
-            raise ValueError(f"k, v: {k.shape[0]}, {v.shape[0]} rows, q has {rows}")
+        rows, hq, hkv = q.shape[0], self.n_q_heads, self.n_kv_heads
+        qp, qs = self._heads(q, "q", rows, hq)
+        kp, ks = self._heads(k, "k", rows, hkv)
+        vp, vs = self._heads(v, "v", rows, hkv)
         if out is None:
-            out = torch.zeros(rows, self.n_q_heads, self.head_dim, dtype=self.dtype, device=self.device)
-        elif out.shape[0] != rows:
-            raise ValueError(f"out: {out.shape[0]} rows, q has {rows}")
-        op, os_ = self._heads(out, "out", self.n_q_heads)
+            out = torch.zeros(rows, hq, self.head_dim, dtype=self.dtype, device=self.device)
+        op, os_ = self._heads(out, "out", rows, hq)
         n_pages, page_size, pool = self._pool(kv_pool, layer)
-        gains = []
-        for t, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
-            if t is not None:
-                _need(t, name, self.dtype, self.device, (self.head_dim,))
-                if t.data_ptr() % 16:
-                    raise ValueError(f"{name}: must be 16-byte aligned")
-            gains.append(t.data_ptr() if t is not None else None)
-        args = _abi.ChunkQkArgs(rows, layer, page_size, n_pages, eps, qs, ks, vs, os_, qp, kp, vp, gains[0], gains[1],
-                                self._ints(row_pos, "row_pos", (rows,)), self._ints(row_slot, "row_slot", (rows,)), op, pool)
-        self._call(self._lib.focus_chunk_qk_norm_rope, args, "focus_chunk_qk_norm_rope", stream)
+        gq = self._gain(q_norm, "q_norm") if q_norm is not None else 0
+        gk = self._gain(k_norm, "k_norm") if k_norm is not None else 0
+        args = _abi.QK_PACK.pack(rows, layer, page_size, n_pages, eps, qs, ks, vs, os_, qp, kp, vp, gq, gk,
+                                 self._ints(row_pos, "row_pos", (rows,)), self._ints(row_slot, "row_slot", (rows,)), op, pool)
+        self._call(1, args, "focus_chunk_qk_norm_rope", stream)
         return out
+
+    def _gain(self, t, name):
+        if not (isinstance(t, torch.Tensor) and t.dtype is self.dtype and t.get_device() == self._index and
+                t.shape == (self.head_dim,) and t.is_contiguous()):
+            _need(t, name, self.dtype, self.device, (self.head_dim,))
+        p = t.data_ptr()
+        if p % 16:
+            raise ValueError(f"{name}: must be 16-byte aligned")
+        return p
 
     def attention(self, q, kv_pool, layer: int, row_offsets, kv_len, page_table, *, max_new: Optional[int] = None,
                   mask_block: int = 1, scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
@@ -176,13 +199,11 @@ class ChunkContext:
         """Attention of the chunk's queries [rows, Hq, d] over the cached keys and values
         (focus_chunk_attention).  `max_new` bounds the rows of a request (default: all rows); a tight bound
         saves work.  mask_block 1 is the causal mask, B the block-causal mask of blocks of B positions."""
-        rows, n = int(q.shape[0]), int(kv_len.shape[0])
-        qp, qs = self._heads(q, "q", self.n_q_heads)
+        rows, n, hq = q.shape[0], kv_len.shape[0], self.n_q_heads
+        qp, qs = self._heads(q, "q", rows, hq)
         if out is None:
-            out = torch.zeros(rows, self.n_q_heads, self.head_dim, dtype=self.dtype, device=self.device)
-        elif out.shape[0] != rows:
-            raise ValueError(f"out: {out.shape[0]} rows, q has {rows}")
-        op, os_ = self._heads(out, "out", self.n_q_heads)
+            out = torch.zeros(rows, hq, self.head_dim, dtype=self.dtype, device=self.device)
+        op, os_ = self._heads(out, "out", rows, hq)
         n_pages, page_size, pool = self._pool(kv_pool, layer)
         if max_new is None:
             max_new = max(rows, 1)
@@ -190,10 +211,10 @@ class ChunkContext:
             scale = 0.0
         elif not scale > 0:
             raise ValueError(f"scale {scale}: must be positive")
-        args = _abi.ChunkAttnArgs(n, rows, max_new, page_size, n_pages, layer, mask_block, scale, qs, os_, qp, pool,
-                                  self._ints(row_offsets, "row_offsets", (n + 1,)), self._ints(kv_len, "kv_len", (n,)),
-                                  self._ints(page_table, "page_table", (n, self.limits.max_pages_per_req)), op)
-        self._call(self._lib.focus_chunk_attention, args, "focus_chunk_attention", stream)
+        args = _abi.ATTN_PACK.pack(n, rows, max_new, page_size, n_pages, layer, mask_block, scale, qs, os_, qp, pool,
+                                   self._ints(row_offsets, "row_offsets", (n + 1,)), self._ints(kv_len, "kv_len", (n,)),
+                                   self._ints(page_table, "page_table", (n, self.limits.max_pages_per_req)), op)
+        self._call(2, args, "focus_chunk_attention", stream)
         return out
 
     # ---- state ------------------------------------------------------------------------------------------
