@@ -20,6 +20,7 @@ namespace {
 
 constexpr int kD = 128;
 constexpr int kKeys = 64;
+constexpr int kUnits = 4;                    // unit descriptors in flight
 constexpr int kHalf = kKeys * 128;           // [64 keys][64 columns] bf16
 constexpr int kStage = 4 * kHalf;            // per page: K lo, K hi, V lo, V hi of S rows; 32 KB in all
 constexpr int kStages = 4;
@@ -108,11 +109,10 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
         uint32_t n = 0, d = 0;        // stages filled, units described
         bool ok = true;
         ChunkWalk<kKeys> wk;
-        auto all_ok = [&](bool x) { return __all_sync(0xffffffffu, x) != 0; };
         // describe the unit and start its query rows on their way
         auto publish = [&](bool live) {
             const uint32_t s = d % kUnits;
-            if (!all_ok(wait_bar(&u_empty[s], ((d / kUnits) & 1u) ^ 1u, a.err))) return false;
+            if (!warp_wait(&u_empty[s], ((d / kUnits) & 1u) ^ 1u, a.err)) return false;
             const int nrow = live ? min(sh.tok, wk.r.n - wk.k * sh.tok) * a.G : 0;
             if (lane == 0) {
                 describe(unit_s[s], wk, rg, sh, live);
@@ -130,26 +130,21 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
             ++d;
             return true;
         };
+        PageWalk pw;
         for (wk.start(a, sh, rg); ok && wk.live(); wk.next(a, sh)) {
+            pw.start(a, wk.b, wk.r.kv, wk.blk0 * ppb);
             ok = publish(true);
-            const int32_t* pt = a.page_table + (size_t)wk.b * a.max_pages;
-            int p0 = wk.blk0 * ppb;
-            int ahead0 = p0, ahead = p0 + lane < a.max_pages ? pt[p0 + lane] : -1;  // table entries ahead0 + lane
-            const int pages = (wk.r.kv + a.S - 1) / a.S;
-            for (int blk = wk.blk0; ok && blk < wk.blk1; ++blk, ++n, p0 += ppb) {
-                if (p0 + ppb > ahead0 + 32) {
-                    ahead0 = p0;
-                    ahead = p0 + lane < a.max_pages ? pt[p0 + lane] : -1;
-                }
+            for (int blk = wk.blk0; ok && blk < wk.blk1; ++blk, ++n, pw.at += ppb) {
+                pw.need(ppb);
                 const uint32_t st = n % kStages;
                 uint32_t bad = 0;
                 int good = 0;
-                for (int p = 0; p < ppb && p0 + p < pages; ++p) {
-                    const int page = __shfl_sync(0xffffffffu, ahead, p0 + p - ahead0);
+                for (int p = 0; p < ppb && pw.in(p); ++p) {
+                    const int page = pw.page(p);
                     if (page >= 0 && page < a.n_pages) ++good;
                     else bad |= ((1u << (a.S / 16)) - 1u) << (p * (a.S / 16));
                 }
-                ok = all_ok(wait_bar(&empty[st], ((n / kStages) & 1u) ^ 1u, a.err));
+                ok = warp_wait(&empty[st], ((n / kStages) & 1u) ^ 1u, a.err);
                 if (!ok) break;
                 if (el) {
                     if (bad) raise_err(a.err, FOCUS_DEVERR_PAGE_ID);
@@ -157,8 +152,8 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
                     mbar_expect_tx(&full[st], (uint32_t)(good * a.S) * 512u);
                 }
                 __syncwarp();
-                for (int p = 0; p < ppb && p0 + p < pages; ++p) {
-                    const int page = __shfl_sync(0xffffffffu, ahead, p0 + p - ahead0);
+                for (int p = 0; p < ppb && pw.in(p); ++p) {
+                    const int page = pw.page(p);
                     if (page >= 0 && page < a.n_pages && el)
                         tma_load_pool(&pool_map, &full[st], ring + st * kStage + p * a.S * 512, 0, 0,
                                       (int)(((long long)page * a.L + a.layer) * 2 * a.Hkv) + wk.g);
@@ -168,8 +163,8 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
         }
         if (ok) publish(false);
         // never leave with copies in flight
-        for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i) wait_bar(&full[i % kStages], (i / kStages) & 1u, a.err);
-        for (uint32_t i = d > kUnits ? d - kUnits : 0; i < d; ++i) wait_bar(&u_full[i % kUnits], (i / kUnits) & 1u, a.err);
+        for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i) warp_wait(&full[i % kStages], (i / kStages) & 1u, a.err);
+        for (uint32_t i = d > kUnits ? d - kUnits : 0; i < d; ++i) warp_wait(&u_full[i % kUnits], (i / kUnits) & 1u, a.err);
         return;
     }
 
@@ -187,7 +182,7 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
     for (uint32_t u = 0;; ++u) {
         // the eight warps go on or stop together: a wait that gave up in one of them alone would leave the others
         // at a named barrier
-        if (!all_agree<32 * kConsumers>(1, wait_bar(&u_full[u % kUnits], (u / kUnits) & 1u, a.err))) break;
+        if (!all_agree<32 * kConsumers>(1, warp_wait(&u_full[u % kUnits], (u / kUnits) & 1u, a.err))) break;
         const UnitDesc& ud = unit_s[u % kUnits];
         const int nb = ud.nb;
         if (nb == 0) break;
@@ -217,7 +212,7 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
         for (int i = 0; i < nb; ++i, ++n) {
             if ((int)(n & 1u) != grp) continue;
             const uint32_t st = n % kStages;
-            alive = __all_sync(0xffffffffu, alive && wait_bar(&full[st], (n / kStages) & 1u, a.err));
+            alive = alive && warp_wait(&full[st], (n / kStages) & 1u, a.err);
             if (!alive) continue;
             const int key0 = (ud.blk0 + i) * kKeys + ks;
             const uint32_t bad = (bad_s[st] >> (ks >> 4)) & 1u;

@@ -3,7 +3,7 @@
 // are split over the CTAs.
 //
 // Unit: request b, KV head g and up to 256 query vectors (token r / G, head r % G) in two tiles of up to
-// 128.  Keys come in blocks of 128 through a ring of five 32 KB slots, K_0 V_0 K_1 V_1 ..., each filled from
+// 128.  Keys come in blocks of 64 through rings of four K and five V slots of 16 KB, each filled from
 // whole pages by TMA (two 64-column halves, 128-byte swizzle).  Per tile t and block i:
 //   S_t = Q_t K_i^T     tcgen05.mma 128 x 128 x 128, both operands in shared memory, into TMEM
 //   softmax             one warpgroup per tile, one thread per query vector: the 128 scores from TMEM,
@@ -37,19 +37,20 @@ constexpr int kD = 128;
 constexpr int kKeys = 64;                     // keys per block
 constexpr int kHalf = kKeys * 128;            // [64 keys][64 columns] bf16: 8 KB
 constexpr int kSlot = 2 * kHalf;              // K or V of one block: 16 KB
-constexpr int kSlots = 9;
+constexpr int kKSlots = 4, kVSlots = 5;       // K is used two blocks ahead of V, V a block longer
+constexpr int kUnits = 4;                     // unit descriptors in flight
 constexpr int kQHalf = 128 * 128;             // [128 query vectors][64 columns]
 constexpr int kQTile = 2 * kQHalf;            // one query tile: 32 KB
-constexpr int kSmem = 2 * kQTile + kSlots * kSlot + 1024;
+constexpr int kSmem = 2 * kQTile + (kKSlots + kVSlots) * kSlot + 1024;
 constexpr int kSoftWarps = 8;                 // 4 per tile: one thread per query vector
-constexpr int kTileThreads = 32 * kSoftWarps + 128;  // then one warp for the copies and one per tile for the MMAs
-constexpr int kCopyWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;  // tile t: warp kMmaWarp + t
+constexpr int kTileThreads = 32 * kSoftWarps + 128;  // then two warps for the copies and one per tile for the MMAs
+constexpr int kCopyWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1, kCopyVWarp = kSoftWarps + 3;  // MMAs of tile t: kMmaWarp + t
 constexpr int kFlags = 16;                    // bad-page flags, one per block in flight
 constexpr float kRaise = 8.f;
 constexpr float kExp1 = 0.69328290f, kExp2 = 0.24221095f, kExp3 = 0.05500893f;
 constexpr int kPolyOf8 = 2;                   // of 8 pairs of weights, those computed on the FMA pipe
 static_assert(kSmem <= 220 * 1024, "shared memory");
-static_assert(kChunkMaxRequests * 8 <= kSlots * kSlot, "the schedule's sums fit in the ring");
+static_assert(kChunkMaxRequests * 8 <= (kKSlots + kVSlots) * kSlot, "the schedule's sums fit in the ring");
 
 __device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* bar, void* dst, int x, int y, int z) {
     asm volatile(
@@ -212,9 +213,11 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
     pdl_trigger();
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* q_s = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* ring = q_s + 2 * kQTile;
-    __shared__ __align__(8) uint64_t q_full, q_empty, kv_full[kSlots], kv_empty[kSlots], s_full[2][2],
-        p_full[2][2], o_full[2], done_bar[2], u_full[kUnits], u_empty[kUnits];
+    uint8_t* k_ring = q_s + 2 * kQTile;
+    uint8_t* v_ring = k_ring + kKSlots * kSlot;
+    __shared__ __align__(8) uint64_t q_full, q_empty, k_full[kKSlots], k_empty[kKSlots], v_full[kVSlots],
+        v_empty[kVSlots], s_full[2][2],
+        p_full[2][2], o_full[2][2], done_bar[2], u_full[kUnits], u_empty[kUnits];
     __shared__ UnitDesc unit_s[kUnits];
     __shared__ uint32_t bad_s[kFlags];  // per block: 16-key groups whose page id is invalid
     __shared__ uint32_t tmem_slot;
@@ -226,21 +229,25 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
     if (threadIdx.x == 0) {
         mbar_init(&q_full, 1);
         mbar_init(&q_empty, 2);  // both tiles' MMA warps
-        for (int s = 0; s < kSlots; ++s) {
-            mbar_init(&kv_full[s], 1);
-            mbar_init(&kv_empty[s], 2);
+        for (int s = 0; s < kKSlots; ++s) {
+            mbar_init(&k_full[s], 1);
+            mbar_init(&k_empty[s], 2);
+        }
+        for (int s = 0; s < kVSlots; ++s) {
+            mbar_init(&v_full[s], 1);
+            mbar_init(&v_empty[s], 2);
         }
         for (int t = 0; t < 2; ++t) {
             for (int b = 0; b < 2; ++b) {
                 mbar_init(&s_full[t][b], 1);
                 mbar_init(&p_full[t][b], 4);  // one arrival per softmax warp
+                mbar_init(&o_full[t][b], 1);  // P V of even / odd blocks complete
             }
-            mbar_init(&o_full[t], 1);
             mbar_init(&done_bar[t], 1);
         }
         for (int s = 0; s < kUnits; ++s) {
             mbar_init(&u_full[s], 1);
-            mbar_init(&u_empty[s], 2 + kSoftWarps);  // the MMA and the softmax warps
+            mbar_init(&u_empty[s], 3 + kSoftWarps);  // the V copies, the MMA and the softmax warps
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -262,86 +269,107 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
 
     const int tpt = 128 / a.G;  // tokens per tile
     const ChunkShape sh{2 * tpt, a.G <= kChunkFewRows ? kChunkFewRows : 0, 0x7fffffff};
-    chunk_schedule<kKeys>(a, sh, min_blocks, reinterpret_cast<long long*>(ring), red, &rg);
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the ring held the schedule's sums
+    chunk_schedule<kKeys>(a, sh, min_blocks, reinterpret_cast<long long*>(k_ring), red, &rg);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the rings held the schedule's sums
     __syncthreads();
 
     // the copy thread walks the range; the others read what it has found
-    auto unit_wait = [&](uint32_t u) { return wait_bar(&u_full[u % kUnits], (u / kUnits) & 1u, a.err); };
+    auto unit_wait = [&](uint32_t u) { return warp_wait(&u_full[u % kUnits], (u / kUnits) & 1u, a.err); };
 
     if (warp >= kSoftWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
-        if (warp == kCopyWarp && lane == 0) {
-            // ---- copies
-            const uint32_t half_q = (uint32_t)(a.G * tpt) * 128u;
-            uint32_t n = 0, u = 0;  // ring slots filled, units
+        if (warp == kCopyWarp || warp == kCopyVWarp) {
+            // ---- copies: one warp walks the range and fetches Q and K, the other follows it and fetches V
+            const bool is_k = warp == kCopyWarp;
+            const int kv = is_k ? 0 : 1, slots = is_k ? kKSlots : kVSlots, ppb = kKeys / a.S;
+            uint8_t* ring = is_k ? k_ring : v_ring;
+            uint64_t *full = is_k ? k_full : v_full, *empty = is_k ? k_empty : v_empty;
+            const uint32_t el = elect_one(), half_q = (uint32_t)(a.G * tpt) * 128u;
+            uint32_t n = 0, u = 0;  // blocks copied, units
+            int st = 0;             // n % slots
+            uint32_t turn = 0;      // n / slots
             bool ok = true;
-            uint32_t blocks = 0, d = 0;
-            ChunkWalk<kKeys> wk;
-            auto publish = [&](bool live) {
-                if (!wait_bar(&u_empty[d % kUnits], ((d / kUnits) & 1u) ^ 1u, a.err)) return false;
-                describe(unit_s[d % kUnits], wk, rg, sh, live);
-                mbar_arrive(&u_full[d % kUnits]);
-                ++d;
-                return true;
-            };
-            for (wk.start(a, sh, rg); ok && wk.live(); wk.next(a, sh), ++u) {
-                if (!publish(true) || !wait_bar(&q_empty, (u & 1u) ^ 1u, a.err)) {
-                    ok = false;
-                    break;
-                }
-                const int two = wk.r.n - wk.k * sh.tok > tpt ? 2 : 1;
-                mbar_expect_tx(&q_full, 2u * half_q * two);
-                for (int t = 0; t < two; ++t)
-                    for (int h = 0; h < 2; ++h)
-                        tma_load_3d(&q_map, &q_full, q_s + t * kQTile + h * kQHalf, h * 64, wk.g * a.G,
-                                    wk.r.row0 + wk.k * sh.tok + t * tpt);
-                const int32_t* pt = a.page_table + (size_t)wk.b * a.max_pages;
-                for (int blk = wk.blk0; ok && blk < wk.blk1; ++blk, ++blocks) {
-                    const int key0 = blk * kKeys;
-                    const int np = (min(kKeys, wk.r.kv - key0) + a.S - 1) / a.S;  // pages (<= 0: none)
-                    int page[kKeys / 16];
+                PageWalk pw;
+            auto blocks_of = [&](int g, int blk0, int nb) {
+                for (int i = 0; ok && i < nb; ++i, ++n, pw.at += ppb) {
+                    pw.need(ppb);
                     uint32_t bad = 0;
                     int good = 0;
-#pragma unroll
-                    for (int p = 0; p < kKeys / 16; ++p) {
-                        if (p < np) {
-                            page[p] = pt[key0 / a.S + p];
-                            if (page[p] < 0 || page[p] >= a.n_pages) {
-                                raise_err(a.err, FOCUS_DEVERR_PAGE_ID);
-                                bad |= ((1u << (a.S / 16)) - 1u) << (p * (a.S / 16));
-                                page[p] = -1;
-                            } else {
-                                ++good;
-                            }
+                    for (int p = 0; p < ppb && pw.in(p); ++p) {
+                        const int page = pw.page(p);
+                        if (page >= 0 && page < a.n_pages) ++good;
+                        else bad |= ((1u << (a.S / 16)) - 1u) << (p * (a.S / 16));
+                    }
+                    ok = warp_wait(&empty[st], (turn & 1u) ^ 1u, a.err);
+                    if (!ok) break;
+                    if (el) {
+                        if (is_k) {
+                            if (bad) raise_err(a.err, FOCUS_DEVERR_PAGE_ID);
+                            bad_s[n % kFlags] = bad;
+                        }
+                        mbar_expect_tx(&full[st], (uint32_t)(good * a.S) * 256u);
+                    }
+                    __syncwarp();
+                    uint8_t* dst = ring + st * kSlot;
+                    for (int p = 0; p < ppb && pw.in(p); ++p) {
+                        const int page = pw.page(p);
+                        if (page >= 0 && page < a.n_pages && el) {
+                            const int x = (int)(((long long)page * a.L + a.layer) * 2 * a.Hkv) + g;
+                            // (the map's box holds both column halves when a page is a whole block)
+                            tma_load_pool(&pool_map, &full[st], dst + p * a.S * 128, 0, kv, x);
+                            if (a.S < kKeys) tma_load_pool(&pool_map, &full[st], dst + kHalf + p * a.S * 128, 1, kv, x);
                         }
                     }
-                    bad_s[blocks % kFlags] = bad;
-                    for (int kv = 0; kv < 2; ++kv, ++n) {
-                        const uint32_t st = n % kSlots;
-                        if (!wait_bar(&kv_empty[st], ((n / kSlots) & 1u) ^ 1u, a.err)) {
-                            ok = false;
-                            break;
-                        }
-                        mbar_expect_tx(&kv_full[st], (uint32_t)(good * a.S) * 256u);
-                        uint8_t* dst = ring + st * kSlot;
-#pragma unroll
-                        for (int p = 0; p < kKeys / 16; ++p) {
-                            if (p < np && page[p] >= 0) {
-                                const int x = (int)(((long long)page[p] * a.L + a.layer) * 2 * a.Hkv) + wk.g;
-                                // (the map's box holds both column halves when a page is a whole block)
-                                tma_load_pool(&pool_map, &kv_full[st], dst + p * a.S * 128, 0, kv, x);
-                                if (a.S < kKeys)
-                                    tma_load_pool(&pool_map, &kv_full[st], dst + kHalf + p * a.S * 128, 1, kv, x);
-                            }
-                        }
+                    __syncwarp();
+                    if (++st == slots) st = 0, ++turn;
+                }
+            };
+            if (is_k) {
+                ChunkWalk<kKeys> wk;
+                uint32_t d = 0;
+                auto publish = [&](bool live) {
+                    if (!warp_wait(&u_empty[d % kUnits], ((d / kUnits) & 1u) ^ 1u, a.err)) return false;
+                    if (lane == 0) {
+                        describe(unit_s[d % kUnits], wk, rg, sh, live);
+                        mbar_arrive(&u_full[d % kUnits]);
                     }
+                    __syncwarp();
+                    ++d;
+                    return true;
+                };
+                for (wk.start(a, sh, rg); ok && wk.live(); wk.next(a, sh)) {
+                    pw.start(a, wk.b, wk.r.kv, wk.blk0 * ppb);
+                    ok = publish(true) && warp_wait(&q_empty, (u & 1u) ^ 1u, a.err);
+                    if (!ok) break;
+                    const int two = wk.r.n - wk.k * sh.tok > tpt ? 2 : 1;
+                    if (el) {
+                        mbar_expect_tx(&q_full, 2u * half_q * two);
+                        for (int t = 0; t < two; ++t)
+                            for (int h = 0; h < 2; ++h)
+                                tma_load_3d(&q_map, &q_full, q_s + t * kQTile + h * kQHalf, h * 64, wk.g * a.G,
+                                            wk.r.row0 + wk.k * sh.tok + t * tpt);
+                    }
+                    __syncwarp();
+                    ++u;
+                    blocks_of(wk.g, wk.blk0, wk.blk1 - wk.blk0);
+                }
+                if (ok) publish(false);
+                if (u > 0) warp_wait(&q_full, (u - 1) & 1u, a.err);
+            } else {
+                for (; ok; ++u) {
+                    ok = unit_wait(u);
+                    if (!ok) break;
+                    const UnitDesc& ud = unit_s[u % kUnits];
+                    const int b = ud.b, g = ud.g, len = ud.kv, blk0 = ud.blk0, nb = ud.nb;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&u_empty[u % kUnits]);
+                    if (nb == 0) break;
+                    pw.start(a, b, len, blk0 * ppb);
+                    blocks_of(g, blk0, nb);
                 }
             }
-            if (ok) publish(false);
             // never leave with copies in flight
-            if (u > 0) wait_bar(&q_full, (u - 1) & 1u, a.err);
-            for (uint32_t i = n > kSlots ? n - kSlots : 0; i < n; ++i) wait_bar(&kv_full[i % kSlots], (i / kSlots) & 1u, a.err);
+            for (uint32_t i = n > (uint32_t)slots ? n - slots : 0; i < n; ++i) warp_wait(&full[i % slots], (i / slots) & 1u, a.err);
         } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
             // ---- MMAs of tile t: S(j + 2) goes out behind P V(j), so the scores of the next block are ready when the
             // softmax has finished this one.  (One warp for both tiles left the tensor core idle while it waited
@@ -350,23 +378,32 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
             constexpr uint32_t idesc_s = idesc_bf16(128, kKeys);
             constexpr uint32_t idesc_o = idesc_bf16(128, kD) | (1u << 16);  // V MN-major
             const uint32_t el = elect_one();
-            const uint64_t q_desc = smem_desc_sw128(smem_u32(q_s + t * kQTile)), k_desc = smem_desc_sw128(smem_u32(ring)),
-                           val_desc = v_desc(smem_u32(ring));
+            const uint64_t q_desc = smem_desc_sw128(smem_u32(q_s + t * kQTile)), k_desc = smem_desc_sw128(smem_u32(k_ring)),
+                           val_desc = v_desc(smem_u32(v_ring));
             const uint32_t s_col = tmem + (uint32_t)t * 128u, o_col = tmem + 256u + (uint32_t)t * 128u;
-            uint32_t n = 0, sc = 0, pc = 0;  // ring slot of the unit's first K; blocks of S, of P
+            // K blocks used and V blocks used (slot and turn of the ring), blocks of S and of P
+            uint32_t ks = 0, kt = 0, vs = 0, vt = 0, sc = 0, pc = 0;
+            auto next_k = [&]() {
+                if (++ks == kKSlots) ks = 0, ++kt;
+            };
+            auto next_v = [&]() {
+                if (++vs == kVSlots) vs = 0, ++vt;
+            };
             // descriptors count 16-byte units
-            auto scores = [&](uint32_t slot) {
-                const uint64_t kd = k_desc + (uint64_t)(slot * (kSlot >> 4));
+            auto scores = [&]() {
+                const uint64_t kd = k_desc + (uint64_t)(ks * (kSlot >> 4));
                 const uint32_t d = s_col + (sc & 1u) * 64u;
 #pragma unroll
                 for (int kk = 0; kk < kD / 16; ++kk)
                     mma_ss(el, d, q_desc + (uint64_t)(((kk >> 2) * kQHalf + (kk & 3) * 32) >> 4),
                            kd + (uint64_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4), idesc_s, kk > 0 ? 1u : 0u);
                 commit_one(el, &s_full[t][sc & 1u]);
-                commit_one(el, &kv_empty[slot]);
+                commit_one(el, &k_empty[ks]);
                 ++sc;
+                next_k();
             };
-            auto full = [&](uint32_t i) { return wait_bar(&kv_full[i % kSlots], (i / kSlots) & 1u, a.err); };
+            auto k_here = [&]() { return warp_wait(&k_full[ks], kt & 1u, a.err); };
+            auto v_here = [&]() { return warp_wait(&v_full[vs], vt & 1u, a.err); };
             bool ok = true;
             for (uint32_t u = 0; ok; ++u) {
                 if (!unit_wait(u)) break;
@@ -378,50 +415,54 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
                 if (!mine) {
                     // a short unit's second tile: give the queries and the ring slots back as they come (waiting for
                     // each, since a parity wait must not be two phases ahead)
-                    if (!wait_bar(&q_full, u & 1u, a.err)) break;
+                    if (!warp_wait(&q_full, u & 1u, a.err)) break;
                     __syncwarp();
                     if (el) mbar_arrive(&q_empty);
-                    for (int j = 0; ok && j < 2 * nb; ++j, ++n) {
-                        ok = full(n);
+                    for (int j = 0; ok && j < nb; ++j) {
+                        ok = k_here() && v_here();
                         __syncwarp();
-                        if (ok && el) mbar_arrive(&kv_empty[n % kSlots]);
+                        if (ok && el) {
+                            mbar_arrive(&k_empty[ks]);
+                            mbar_arrive(&v_empty[vs]);
+                        }
+                        next_k();
+                        next_v();
                     }
                     continue;
                 }
-                if (!wait_bar(&q_full, u & 1u, a.err)) break;
+                if (!warp_wait(&q_full, u & 1u, a.err)) break;
                 for (int j = 0; ok && j < 2 && j < nb; ++j) {
-                    ok = full(n + 2 * j);
+                    ok = k_here();
                     if (!ok) break;
                     tc_fence_after();
-                    scores((n + 2 * j) % kSlots);
+                    scores();
                 }
                 if (nb <= 2) commit_one(el, &q_empty);
                 for (int j = 0; ok && j < nb; ++j) {
-                    const uint32_t vs = n + 2 * j + 1, kn = n + 2 * j + 4, b = pc & 1u;
-                    const bool more = j + 2 < nb;
-                    ok = full(vs) && wait_bar(&p_full[t][b], (pc >> 1) & 1u, a.err);
+                    const uint32_t b = pc & 1u;
+                    ok = v_here() && warp_wait(&p_full[t][b], (pc >> 1) & 1u, a.err);
                     if (!ok) break;
                     ++pc;
                     tc_fence_after();
-                    const uint64_t vd = val_desc + (uint64_t)((vs % kSlots) * (kSlot >> 4));
+                    const uint64_t vd = val_desc + (uint64_t)(vs * (kSlot >> 4));
 #pragma unroll
                     for (int kk = 0; kk < kKeys / 16; ++kk)
                         mma_ts(el, o_col, s_col + b * 64u + kk * 8, vd + (uint64_t)(kk * (2048 >> 4)), idesc_o,
                                (j > 0 || kk > 0) ? 1u : 0u);
-                    commit_one(el, &o_full[t]);
-                    commit_one(el, &kv_empty[vs % kSlots]);
-                    if (more) {
-                        ok = full(kn);
+                    commit_one(el, &o_full[t][b]);
+                    commit_one(el, &v_empty[vs]);
+                    next_v();
+                    if (j + 2 < nb) {
+                        ok = k_here();
                         if (!ok) break;
                         tc_fence_after();
-                        scores(kn % kSlots);
+                        scores();
                     }
                     if (j + 3 == nb) commit_one(el, &q_empty);  // the unit's last scores have been issued
                 }
-                n += 2 * nb;
             }
             commit_one(el, &done_bar[t]);
-            wait_bar(&done_bar[t], 0u, a.err);
+            warp_wait(&done_bar[t], 0u, a.err);
             __syncwarp();
         }
     } else {
@@ -431,8 +472,12 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
         const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t s_addr = lane_base + (uint32_t)(t * 128), o_addr = lane_base + 256u + (uint32_t)(t * 128);
         const float sl2 = a.scale * 1.4426950408889634f;
-        uint32_t blocks = 0, sc = 0;  // blocks (V of block j is in ring slot 2 j + 1), blocks of this tile
+        uint32_t blocks = 0, sc = 0;  // blocks (V of block j is in V slot j), blocks of this tile
         bool alive = true;
+        // P V of this tile's block j is complete.  Asked for the last block whose P has been handed over, or the one
+        // before it: each of the two barriers is then at this phase or has just left it (the P V two blocks back is
+        // complete, since the scores issued behind it have arrived), so the parity is unambiguous.
+        auto o_wait = [&](uint32_t j) { return warp_wait(&o_full[t][j & 1u], (j >> 1) & 1u, a.err); };
         for (uint32_t u = 0;; ++u) {
             // the tile's warps go on or stop together: a wait that gave up in one of them alone would leave the
             // others at a named barrier
@@ -458,9 +503,8 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
             float m = -CUDART_INF_F, l = 0.f;
             for (int i = 0; i < nb; ++i, ++blocks, key0 += kKeys) {
                 const uint32_t b = sc & 1u;
-                alive = alive && wait_bar(&s_full[t][b], (sc >> 1) & 1u, a.err);
+                alive = alive && warp_wait(&s_full[t][b], (sc >> 1) & 1u, a.err);
                 ++sc;
-                alive = __all_sync(0xffffffffu, alive);
                 if (!alive) continue;
                 tc_fence_after();
                 uint32_t s[64];
@@ -494,9 +538,8 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
                     m = cm;
                 }
                 if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
-                    // O has to hold the previous block's P V (its barrier is at most one phase past this one, since
-                    // this block's P V waits for the P below)
-                    alive = __all_sync(0xffffffffu, wait_bar(&o_full[t], (sc - 2) & 1u, a.err));
+                    // O has to hold the previous block's P V
+                    alive = o_wait(sc - 2);
                     tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < kD; c += 32) {
@@ -512,11 +555,11 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
                 // V rows of keys that do not exist may hold anything (a page's tail, an old copy): their weight
                 // is 0, so make them 0 as well
                 if (key0 + kKeys > kv || bad != 0) {
-                    const uint32_t vs = 2 * blocks + 1;
-                    alive = __all_sync(0xffffffffu, wait_bar(&kv_full[vs % kSlots], (vs / kSlots) & 1u, a.err));
+                    const uint32_t vs = blocks % kVSlots;
+                    alive = warp_wait(&v_full[vs], (blocks / kVSlots) & 1u, a.err);
                     const int key = r & 63;
                     if (key0 + key >= kv || ((bad >> (key >> 4)) & 1u)) {
-                        uint8_t* vr = ring + (vs % kSlots) * kSlot + (r >> 6) * kHalf + key * 128;
+                        uint8_t* vr = v_ring + vs * kSlot + (r >> 6) * kHalf + key * 128;
 #pragma unroll
                         for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(vr + 16 * c) = make_uint4(0, 0, 0, 0);
                     }
@@ -543,11 +586,7 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
                 const uint64_t sum = add2(sum0, sum1);
                 l += __uint_as_float((uint32_t)sum) + __uint_as_float((uint32_t)(sum >> 32));
             }
-            // the last scores only promise the P V two blocks back; a parity wait must not be two phases ahead, so
-            // wait for the last but one as well
-            alive = alive && (sc < 2 || wait_bar(&o_full[t], (sc - 2) & 1u, a.err)) &&
-                    wait_bar(&o_full[t], (sc - 1) & 1u, a.err);
-            alive = __all_sync(0xffffffffu, alive);
+            alive = alive && o_wait(sc - 1);
             tc_fence_after();
             bf16* dst = reinterpret_cast<bf16*>(a.out) + (long long)(ud.row0 + tok0 + rt) * a.out_stride +
                         (ud.g * a.G + r - rt * a.G) * kD;

@@ -12,8 +12,6 @@ using tc::mbar_expect_tx;
 using tc::mbar_init;
 using tc::smem_u32;
 
-constexpr int kUnits = 4;  // unit descriptors in flight
-
 // As tc::mbar_wait, but the clock is read only every 64 failed tries: the waiting warps share their SM
 // quarter's issue slots with the ones that work.
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, int* err) {
@@ -29,6 +27,12 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, int* er
             return false;
         }
     }
+}
+
+// The same for a whole warp.  Its lanes leave together: one that ran on alone could pass the barrier's next two
+// phases while the others still look for this one, and they would then wait for a parity that has come and gone.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* err) {
+    return __all_sync(0xffffffffu, wait_bar(bar, parity, err)) != 0;
 }
 
 // N threads meet at named barrier `id`; all_agree also tells whether `ok` held in every one of them.
@@ -47,7 +51,7 @@ template <int N> __device__ __forceinline__ bool all_agree(int id, bool ok) {
 // One piece of a unit, written by the copy thread as it reaches it and read by the other roles.
 struct UnitDesc {
     int row0, n, kv;          // the request
-    int g, tok0;              // KV head, first token
+    int b, g, tok0;           // request number, KV head, first token
     int blk0, nb;             // key blocks of the piece (nb = 0: no more units)
     int c0, c1, slot0;        // CTAs that hold pieces (c0 = -1: the whole unit is here), scratch slot of c0's
 };
@@ -60,6 +64,7 @@ __device__ __forceinline__ void describe(UnitDesc& ud, const ChunkWalk<KEYS>& wk
     ud.row0 = wk.r.row0;
     ud.n = wk.r.n;
     ud.kv = wk.r.kv;
+    ud.b = wk.b;
     ud.g = wk.g;
     ud.tok0 = wk.k * sh.tok;
     ud.blk0 = wk.blk0;
@@ -70,8 +75,9 @@ __device__ __forceinline__ void describe(UnitDesc& ud, const ChunkWalk<KEYS>& wk
 
 // The pool's rows of 128 columns for TMA, as (64 columns, S tokens, column half, K / V, x) with
 // x = (page L + layer) 2 Hkv + head: one copy takes a page's K or V of a head, or both, as `halves` x `kvs`
-// tiles of [S][64 columns] with 128-byte rows, swizzled.  A copy instruction costs its issuing thread some
-// 200 cycles whatever it moves, so the fewest and largest are used.
+// tiles of [S][64 columns] with 128-byte rows, swizzled.  A copy instruction takes its issuing warp
+// 65 to 100 cycles whatever it moves (measured; lanes of one warp take turns, warps do not), so the fewest
+// and largest are used.
 inline bool make_pool_map(CUtensorMap* m, const ChunkAttnDev& a, int halves, int kvs) {
     auto fn = tc::encode_fn();
     if (!fn) return false;
@@ -90,6 +96,31 @@ __device__ __forceinline__ void tma_load_pool(const CUtensorMap* map, uint64_t* 
         ::"r"(smem_u32(dst)), "l"(map), "r"(smem_u32(bar)), "r"(0), "r"(half), "r"(kv), "r"(x)
         : "memory");
 }
+
+// The pages of one key block at a time, for a whole warp: the next 32 entries of the request's table row sit in
+// the lanes, so a block's ids cost a shuffle, not a load.
+struct PageWalk {
+    const int32_t* pt;
+    int pages, max_pages, at, ahead0, ahead;  // pages that hold keys, row length, next entry, entries ahead0 + lane
+    __device__ __forceinline__ void start(const ChunkAttnDev& a, int b, int kv, int first) {
+        pt = a.page_table + (size_t)b * a.max_pages;
+        pages = (kv + a.S - 1) / a.S;
+        max_pages = a.max_pages;
+        at = first;
+        load();
+    }
+    __device__ __forceinline__ void load() {
+        const int i = at + (int)(threadIdx.x & 31);
+        ahead0 = at;
+        ahead = i < max_pages ? pt[i] : -1;
+    }
+    // entry `at + p` of the block whose `ppb` entries start at `at` (call need() first)
+    __device__ __forceinline__ void need(int ppb) {
+        if (at + ppb > ahead0 + 32) load();
+    }
+    __device__ __forceinline__ int page(int p) const { return __shfl_sync(0xffffffffu, ahead, at + p - ahead0); }
+    __device__ __forceinline__ bool in(int p) const { return at + p < pages; }
+};
 
 // One lane of a converged warp.
 __device__ __forceinline__ uint32_t elect_one() {
