@@ -1,11 +1,14 @@
 // Pages, rows and cache slots of a chunk from the request lengths, in one launch.
 //
-// Three sums over the requests decide everything: rows asked for (does the row buffer hold them), pages
-// needed by those (does the free list), rows of the placed ones (the row offsets).  Each CTA runs the three
-// scans itself over all requests (they are a few hundred integers) and then writes its own slice of the
-// rows and every gridDim-th request's new pages: no CTA waits for another, and a row whose page is new
-// takes it from the free list, not from the table another CTA is writing.  Bound: latency of two dependent
-// loads and the scan for small batches, the 12 bytes written per row for large ones.
+// Sums over the requests decide everything: rows asked for (does the row buffer hold them), pages needed by those
+// (does the free list), rows of the placed ones (the row offsets).  Each CTA runs the scans itself over all
+// requests -- a few hundred integers, a run of consecutive ones per thread -- and then writes its own slice of the
+// rows: no CTA waits for another.  When everything fits, which the first scan tells, it is the only one.  A row
+// whose page is new takes it from the free list, not from the table another CTA is writing, and the row that
+// starts a new page writes its table entry (a new page always starts inside the chunk).
+//
+// Bound: for small batches the latency of the launch, two dependent loads and the scan (32 single tokens: XX us);
+// for large ones the 12 bytes written per row.
 #include "chunk.h"
 
 namespace focus {
@@ -13,6 +16,35 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kRowsPerCta = 1024;
+
+// Inclusive scan of x and y over the block; the totals in tx, ty.  `red` holds 2 x 8 long longs; two barriers.
+__device__ __forceinline__ void block_scan2(long long& x, long long& y, long long& tx, long long& ty, long long (*red)[8]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) {
+            x += u;
+            y += v;
+        }
+    }
+    __syncthreads();  // red has been read by the scan before
+    if (lane == 31) {
+        red[0][warp] = x;
+        red[1][warp] = y;
+    }
+    __syncthreads();
+    tx = ty = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w == warp) {
+            x += tx;
+            y += ty;
+        }
+        tx += red[0][w];
+        ty += red[1][w];
+    }
+}
 
 __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(ChunkPlanDev a) {
     pdl_entry();
@@ -22,8 +54,8 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(ChunkPlanDev a) {
     int32_t* off = sm;                // [N + 1] row offsets
     int32_t* pre = off + N + 1;       // [N] prefix lengths
     int32_t* first = pre + N;         // [N] free-list index of a request's first new page
-    __shared__ long long red[3][kThreads / 32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ long long red[2][8];
+    const int tid = threadIdx.x;
     const bool lead = blockIdx.x == 0;
     const long long cap = (long long)a.max_pages * S;
 
@@ -32,73 +64,96 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(ChunkPlanDev a) {
     const int avail = head_ok ? p.n_free - head : 0;
     if (!head_ok && lead && tid == 0) raise_err(a.err, FOCUS_DEVERR_PAGE_ID);
 
-    // running totals over the earlier requests: rows asked, pages needed, rows placed, pages taken
-    long long c_ask = 0, c_need = 0, c_rows = 0, c_taken = 0;
-    for (int b0 = 0; b0 < N; b0 += kThreads) {
-        const int b = b0 + tid;
-        int pl = 0, n = 0;
-        bool valid = false;
-        if (b < N) {
-            pl = p.prefix_len[b];
-            n = p.new_len[b];
-            valid = pl >= 0 && n >= 0 && (long long)pl + n <= cap;
-            if (!valid && lead) raise_err(a.err, FOCUS_DEVERR_PREFIX);
+    const int per = (N + kThreads - 1) / kThreads, b0 = min(N, tid * per), b1 = min(N, b0 + per);
+    // request b's lengths (n = -1: out of range, no rows) and the pages n new tokens need
+    auto lens = [&](int b, int& pl, int& n) {
+        pl = p.prefix_len[b];
+        n = p.new_len[b];
+        if (pl < 0 || n < 0 || (long long)pl + n > cap) n = -1;
+    };
+    auto need = [&](int pl, int n) { return (pl + n + S - 1) / S - (pl + S - 1) / S; };
+    auto write = [&](int b, int pl, int rows, long long row, long long page) {
+        off[b] = (int)row;
+        pre[b] = pl;
+        first[b] = head + (int)page;
+        if (lead) {
+            p.row_offsets[b] = (int)row;
+            p.kv_len[b] = pl + rows;
         }
-        auto scan = [&](long long v, int which, long long& total) {
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long u = __shfl_up_sync(0xffffffffu, v, o);
-                if (lane >= o) v += u;
-            }
-            if (lane == 31) red[which][warp] = v;
-            __syncthreads();
-            total = 0;
-#pragma unroll
-            for (int w = 0; w < kThreads / 32; ++w) {
-                if (w < warp) v += red[which][w];
-                total += red[which][w];
-            }
-            return v;
-        };
-        long long t_ask, t_need, t_rows;
-        const long long ask = c_ask + scan(valid ? n : 0, 0, t_ask);
-        const bool rows_ok = valid && (n == 0 || ask <= p.max_rows);
-        const int have = rows_ok ? (pl + S - 1) / S : 0;
-        const int need = rows_ok ? (pl + n + S - 1) / S - have : 0;
-        const long long upto = c_need + scan(need, 1, t_need);
-        const bool placed = rows_ok && (need == 0 || upto <= avail);
-        const int rows = placed ? n : 0;
-        const long long end = c_rows + scan(rows, 2, t_rows);
-        if (b < N) {
-            off[b] = (int)(end - rows);
-            pre[b] = pl;
-            first[b] = placed && need > 0 ? head + (int)(upto - need) : head;
-            if (lead) {
-                p.row_offsets[b] = (int)(end - rows);
-                p.kv_len[b] = pl + rows;
-            }
+    };
+    long long ask = 0, want = 0, all_ask, all_want;
+    int pl1 = 0, n1 = 0;  // the thread's lengths when it has one request
+    for (int b = b0; b < b1; ++b) {
+        lens(b, pl1, n1);
+        if (n1 < 0 && lead) raise_err(a.err, FOCUS_DEVERR_PREFIX);
+        if (n1 > 0) {
+            ask += n1;
+            want += need(pl1, n1);
         }
-        // pages taken: the needs of the placed requests are a prefix of all needs
-        long long mine = placed && need > 0 ? upto : 0;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const long long u = __shfl_xor_sync(0xffffffffu, mine, o);
-            mine = u > mine ? u : mine;
-        }
-        __syncthreads();  // red has been read
-        if (lane == 0) red[0][warp] = mine;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) c_taken = red[0][w] > c_taken ? red[0][w] : c_taken;
-        c_ask += t_ask;
-        c_need += t_need;
-        c_rows += t_rows;
-        __syncthreads();  // red is reused by the next round
     }
-    const int total = (int)c_rows;
+    long long ask_end = ask, want_end = want;
+    block_scan2(ask_end, want_end, all_ask, all_want, red);
+    long long total = all_ask, taken = all_want;
+    if (all_ask <= p.max_rows && all_want <= avail) {
+        // everything fits: what was asked for is what is placed
+        long long row = ask_end - ask, page = want_end - want;
+        for (int b = b0; b < b1; ++b) {
+            if (per > 1) lens(b, pl1, n1);
+            const int rows = max(n1, 0);
+            write(b, pl1, rows, row, page);
+            row += rows;
+            if (rows > 0) page += need(pl1, rows);
+        }
+    } else {
+        // the row test over all requests, then the page test over those that passed it, then the placed ones' rows
+        auto rows_fit = [&](int n, long long& run) {
+            if (n <= 0) return n == 0;
+            run += n;
+            return run <= p.max_rows;
+        };
+        long long run = ask_end - ask, w = 0, dummy = 0, tw, td;
+        for (int b = b0; b < b1; ++b) {
+            int pl, n;
+            lens(b, pl, n);
+            if (rows_fit(n, run)) w += need(pl, n);
+        }
+        long long w_end = w;
+        block_scan2(w_end, dummy, tw, td, red);
+        auto placed = [&](int pl, int n, long long& r, long long& pg, int& pages) {
+            if (!rows_fit(n, r)) return false;
+            pages = need(pl, n);
+            pg += pages;
+            return pages == 0 || pg <= avail;
+        };
+        long long mine = 0, got = 0;
+        run = ask_end - ask;
+        long long pg = w_end - w;
+        for (int b = b0; b < b1; ++b) {
+            int pl, n, pages = 0;
+            lens(b, pl, n);
+            if (placed(pl, n, run, pg, pages)) {
+                mine += n;
+                got += pages;
+            }
+        }
+        long long mine_end = mine, got_end = got;
+        block_scan2(mine_end, got_end, total, taken, red);
+        run = ask_end - ask;
+        pg = w_end - w;
+        long long row = mine_end - mine, page = got_end - got;
+        for (int b = b0; b < b1; ++b) {
+            int pl, n, pages = 0;
+            lens(b, pl, n);
+            if (!placed(pl, n, run, pg, pages)) n = pages = 0;
+            write(b, pl, n, row, page);
+            row += n;
+            page += pages;
+        }
+    }
+    const int rows_all = (int)total;
     if (tid == 0) {
-        off[N] = total;
-        if (lead) p.row_offsets[N] = total;
+        off[N] = rows_all;
+        if (lead) p.row_offsets[N] = rows_all;
     }
     __syncthreads();
 
@@ -107,19 +162,10 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(ChunkPlanDev a) {
         raise_err(a.err, FOCUS_DEVERR_PAGE_ID);
         return -1;
     };
-    // new pages of every gridDim-th request
-    for (int b = blockIdx.x; b < N; b += gridDim.x) {
-        const int n = off[b + 1] - off[b];
-        if (n <= 0) continue;
-        const int have = (pre[b] + S - 1) / S, all = (pre[b] + n + S - 1) / S;
-        for (int i = have + tid; i < all; i += kThreads)
-            p.page_table[(size_t)b * a.max_pages + i] = checked(p.free_pages[first[b] + i - have]);
-    }
-    // this CTA's rows
-    const int r1 = min(p.max_rows, (int)(blockIdx.x + 1) * kRowsPerCta);
+    const int r1 = (int)min((long long)p.max_rows, (long long)(blockIdx.x + 1) * kRowsPerCta);
     for (int r = blockIdx.x * kRowsPerCta + tid; r < r1; r += kThreads) {
         int req = -1, pos = -1, slot = -1;
-        if (r < total) {
+        if (r < rows_all) {
             int lo = 0, hi = N;  // largest b with off[b] <= r: it has rows, since off[b + 1] > r
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
@@ -129,8 +175,9 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(ChunkPlanDev a) {
             req = lo;
             pos = pre[lo] + r - off[lo];
             const int i = pos / S, have = (pre[lo] + S - 1) / S;
-            const int page = checked(i < have ? p.page_table[(size_t)lo * a.max_pages + i]
-                                              : p.free_pages[first[lo] + i - have]);
+            int32_t* entry = p.page_table + (size_t)lo * a.max_pages + i;
+            const int page = checked(i < have ? *entry : p.free_pages[first[lo] + i - have]);
+            if (i >= have && pos == i * S) *entry = page;
             slot = page < 0 ? -1 : page * S + pos - i * S;
         }
         p.row_req[r] = req;
@@ -138,11 +185,15 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(ChunkPlanDev a) {
         p.row_slot[r] = slot;
     }
     // free_next may be free_head: it is written once every CTA has read the head
-    __syncthreads();
-    if (tid == 0) {
-        __threadfence();
-        if (atomicInc(reinterpret_cast<unsigned*>(a.arrivals), gridDim.x - 1) == gridDim.x - 1)
-            *p.free_next = head + (int)c_taken;
+    if (gridDim.x == 1) {
+        if (tid == 0) *p.free_next = head + (int)taken;
+    } else {
+        __syncthreads();
+        if (tid == 0) {
+            __threadfence();
+            if (atomicInc(reinterpret_cast<unsigned*>(a.arrivals), gridDim.x - 1) == gridDim.x - 1)
+                *p.free_next = head + (int)taken;
+        }
     }
 }
 
@@ -155,7 +206,7 @@ bool configure_chunk_plan_kernel() {
 }
 
 int launch_chunk_plan(const ChunkPlanDev& a, cudaStream_t s) {
-    const int ctas = a.p.max_rows > kRowsPerCta ? (a.p.max_rows + kRowsPerCta - 1) / kRowsPerCta : 1;
+    const int ctas = a.p.max_rows > kRowsPerCta ? (int)(((long long)a.p.max_rows + kRowsPerCta - 1) / kRowsPerCta) : 1;
     return launched(launch_pdl(chunk_plan_kernel, dim3(ctas), dim3(kThreads), (3 * a.p.n_requests + 1) * 4, s, 0, a));
 }
 

@@ -15,6 +15,7 @@ namespace focus {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kAhead = 1;  // groups of heads whose loads are in flight while one is turned
 
 template <typename T, int V> struct Pack;  // 16 bytes
 template <> struct Pack<bf16, 8> {
@@ -51,11 +52,12 @@ template <> struct Pack<float, 4> {
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) chunk_qk_kernel(ChunkQkDev a, int warps_per_row) {
+__global__ void __launch_bounds__(kThreads, 6) chunk_qk_kernel(ChunkQkDev a, int warps_per_row) {
     constexpr int V = 16 / (int)sizeof(T);      // values per access
     constexpr int LPH = D / 2 / V;              // lanes per head
     constexpr int HPW = 32 / LPH;               // heads a warp works on at once
     using P = Pack<T, V>;
+    __shared__ __align__(16) float cos_s[kThreads / 32][D / 2], sin_s[kThreads / 32][D / 2];
     pdl_entry();
     const focus_chunk_qk& p = a.p;
     const int gw = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -70,73 +72,99 @@ __global__ void __launch_bounds__(kThreads) chunk_qk_kernel(ChunkQkDev a, int wa
     }
     const int page = slot < 0 ? 0 : slot / p.page_size, at = slot < 0 ? 0 : slot - page * p.page_size;
     const int hl = lane % LPH, hw = lane / LPH, c0 = hl * V;
-    float cn[V], sn[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const double t = (double)pos * a.freq_over_pi[c0 + i];
-        sincospif((float)(t - 2.0 * rint(0.5 * t)), &sn[i], &cn[i]);
-    }
-    const int heads = a.Hq + 2 * a.Hkv;
-    const T* q = reinterpret_cast<const T*>(p.q) + (long long)row * p.q_stride;
-    const T* k = reinterpret_cast<const T*>(p.k) + (long long)row * p.k_stride;
-    const T* v = reinterpret_cast<const T*>(p.v) + (long long)row * p.v_stride;
-    T* out = reinterpret_cast<T*>(p.q_out) + (long long)row * p.out_stride;
-    T* pool = reinterpret_cast<T*>(p.kv_pool);
-    const int step = warps_per_row * HPW;
-#pragma unroll 4
-    for (int h0 = part * HPW; h0 < heads; h0 += step) {
-        const int h = h0 + hw;
-        const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.Hkv, live = h < heads;
-        const T* src = is_q ? q + h * D : is_k ? k + (h - a.Hq) * D : v + (h - a.Hq - a.Hkv) * D;
-        P lo, hi;
-        lo.u = hi.u = make_uint4(0, 0, 0, 0);
-        if (live) {
-            lo.u = *reinterpret_cast<const uint4*>(src + c0);
-            hi.u = *reinterpret_cast<const uint4*>(src + D / 2 + c0);
+    // groups of HPW heads: the query heads', the key heads', the value heads' (none straddles)
+    const int gq = (a.Hq + HPW - 1) / HPW, gk = (a.Hkv + HPW - 1) / HPW, groups = gq + 2 * gk;
+    const T* q = reinterpret_cast<const T*>(p.q) + (long long)row * p.q_stride + c0;
+    const T* k = reinterpret_cast<const T*>(p.k) + (long long)row * p.k_stride + c0;
+    const T* v = reinterpret_cast<const T*>(p.v) + (long long)row * p.v_stride + c0;
+    P lo[kAhead], hi[kAhead];
+    auto fetch = [&](int g, P& l, P& u) {
+        const int kind = g < gq ? 0 : g < gq + gk ? 1 : 2;
+        const int h = (kind == 0 ? g : kind == 1 ? g - gq : g - gq - gk) * HPW + hw;
+        const T* src = (kind == 0 ? q : kind == 1 ? k : v) + h * D;
+        l.u = u.u = make_uint4(0, 0, 0, 0);
+        if (g < groups && h < (kind == 0 ? a.Hq : a.Hkv)) {
+            l.u = *reinterpret_cast<const uint4*>(src);
+            u.u = *reinterpret_cast<const uint4*>(src + D / 2);
         }
-        const T* gain = reinterpret_cast<const T*>(is_q ? p.q_norm : p.k_norm);
-        const bool norm = (is_q || is_k) && gain != nullptr;
-        float x[V], y[V];
-        lo.get(x);
-        hi.get(y);
-        float ss = 0.f;
+    };
 #pragma unroll
-        for (int i = 0; i < V; ++i) ss = fmaf(x[i], x[i], fmaf(y[i], y[i], ss));
+    for (int i = 0; i < kAhead; ++i) fetch(part + i * warps_per_row, lo[i], hi[i]);
+
+    // the row's angles, D / 64 pairs per lane, to shared memory
+    const int warp = threadIdx.x >> 5;
 #pragma unroll
-        for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (is_q || is_k) {
-            if (norm) {
-                const float inv = rsqrtf(ss / D + p.eps);
+    for (int i = lane; i < D / 2; i += 32) {
+        const double t = (double)pos * a.freq_over_pi[i];
+        float s, c;
+        sincospif((float)(t - 2.0 * rint(0.5 * t)), &s, &c);
+        cos_s[warp][i] = c;
+        sin_s[warp][i] = s;
+    }
+    __syncwarp();
+    T* out = reinterpret_cast<T*>(p.q_out) + (long long)row * p.out_stride + c0;
+    T* pool = reinterpret_cast<T*>(p.kv_pool) +
+              (((size_t)page * a.L + p.layer) * 2 * a.Hkv * p.page_size + at) * D + c0;  // K of head 0 at this slot
+    const size_t head_step = (size_t)p.page_size * D;
+    auto turn = [&](int g, P& l, P& u) {
+        const int kind = g < gq ? 0 : g < gq + gk ? 1 : 2;
+        const int h = (kind == 0 ? g : kind == 1 ? g - gq : g - gq - gk) * HPW + hw;
+        if (kind < 2) {
+            float x[V], y[V];
+            l.get(x);
+            u.get(y);
+            const T* gain = reinterpret_cast<const T*>(kind == 0 ? p.q_norm : p.k_norm);
+            if (gain != nullptr) {
                 P gl, gh;
                 gl.u = __ldg(reinterpret_cast<const uint4*>(gain + c0));
                 gh.u = __ldg(reinterpret_cast<const uint4*>(gain + D / 2 + c0));
+                float ss = 0.f, st = 0.f;
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    ss = fmaf(x[j], x[j], ss);
+                    st = fmaf(y[j], y[j], st);
+                }
+                ss += st;
+#pragma unroll
+                for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                const float inv = rsqrtf(ss * (1.f / D) + p.eps);
                 float g0[V], g1[V];
                 gl.get(g0);
                 gh.get(g1);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    x[i] *= inv * g0[i];
-                    y[i] *= inv * g1[i];
+                for (int j = 0; j < V; ++j) {
+                    x[j] *= inv * g0[j];
+                    y[j] *= inv * g1[j];
                 }
             }
             float r0[V], r1[V];
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                r0[i] = x[i] * cn[i] - y[i] * sn[i];
-                r1[i] = y[i] * cn[i] + x[i] * sn[i];
+            for (int j = 0; j < V; j += 4) {
+                const float4 c4 = *reinterpret_cast<const float4*>(&cos_s[warp][c0 + j]);
+                const float4 s4 = *reinterpret_cast<const float4*>(&sin_s[warp][c0 + j]);
+                const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    r0[j + e] = x[j + e] * c[e] - y[j + e] * s[e];
+                    r1[j + e] = y[j + e] * c[e] + x[j + e] * s[e];
+                }
             }
-            lo.set(r0);
-            hi.set(r1);
+            l.set(r0);
+            u.set(r1);
         }
-        if (!live) continue;
-        T* dst = out + h * D;
-        if (!is_q) {
-            if (slot < 0) continue;
-            const int kv = is_k ? 0 : 1, g = h - a.Hq - kv * a.Hkv;
-            dst = pool + (((((size_t)page * a.L + p.layer) * 2 + kv) * a.Hkv + g) * p.page_size + at) * D;
+        if (h >= (kind == 0 ? a.Hq : a.Hkv) || (kind > 0 && slot < 0)) return;
+        T* dst = kind == 0 ? out + h * D : pool + (h + (kind == 2 ? a.Hkv : 0)) * head_step;
+        *reinterpret_cast<uint4*>(dst) = l.u;
+        *reinterpret_cast<uint4*>(dst + D / 2) = u.u;
+    };
+    for (int g = part; g < groups; g += kAhead * warps_per_row) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int gi = g + i * warps_per_row;
+            if (gi >= groups) break;  // (the whole warp)
+            turn(gi, lo[i], hi[i]);
+            fetch(gi + kAhead * warps_per_row, lo[i], hi[i]);
         }
-        *reinterpret_cast<uint4*>(dst + c0) = lo.u;
-        *reinterpret_cast<uint4*>(dst + D / 2 + c0) = hi.u;
     }
 }
 
@@ -144,7 +172,7 @@ __global__ void __launch_bounds__(kThreads) chunk_qk_kernel(ChunkQkDev a, int wa
 
 template <typename T, int D> int launch_chunk_qk(const ChunkQkDev& a, cudaStream_t s) {
     constexpr int HPW = 32 / (D / 2 / (16 / (int)sizeof(T)));
-    const int groups = (a.Hq + 2 * a.Hkv + HPW - 1) / HPW;
+    const int groups = (a.Hq + HPW - 1) / HPW + 2 * ((a.Hkv + HPW - 1) / HPW);
     // one warp per row once the rows fill the SMs (32 warps each); fewer rows are shared by several warps
     const int fill = kChunkCtas * 32;
     int wpr = a.p.rows >= fill ? 1 : (fill + a.p.rows - 1) / a.p.rows;
