@@ -35,6 +35,7 @@ struct ChunkAttnDev {
     long long q_stride, out_stride;  // elements
     int N, rows, max_new, Hq, Hkv, G, L, layer, S, n_pages, max_pages, mask_block;
     float scale;
+    bool small_walk;  // the launch's key blocks, and their products with the CTA count, fit 31 bits
     // scratch of units whose key walk is split over CTAs: slot 2c / 2c + 1 is CTA c's first / last piece
     float* part_o;
     float* part_ml;

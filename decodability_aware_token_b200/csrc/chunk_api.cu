@@ -244,6 +244,8 @@ int focus_chunk_attention(focus_chunk_ctx* c, const focus_chunk_attn* p, void* s
     // a block that holds every position a request can reach: the mask is the same, the products fit
     a.mask_block = p->mask_block < max_kv ? p->mask_block : (int)max_kv;
     a.scale = p->scale > 0.f ? p->scale : 1.f / sqrtf((float)c->cfg.head_dim);
+    // (a unit is at least one row of one request and a key block at least 32 keys)
+    a.small_walk = (double)hkv * ((double)p->rows + p->n_requests) * ((double)max_kv / 32 + 1) < 2147483648.0;
     a.part_o = c->part_o;
     a.part_ml = c->part_ml;
     a.counters = c->counters;

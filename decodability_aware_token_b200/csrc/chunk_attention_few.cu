@@ -4,7 +4,7 @@
 //
 // Bound by memory: each cached key and value is read once (64 Hkv d bytes ... per 16-key step 8 KB), so the design
 // is a copy that never stops.  One CTA per SM walks its equal share of the batch's key blocks (chunk_work.cuh);
-// one warp issues the pages of 64-key blocks by TMA into a ring of four 32 KB stages and runs on across unit
+// one warp issues the pages of 64-key blocks by TMA into a ring of six 32 KB stages and runs on across unit
 // ends; eight warps consume, four per block, 16 keys each.  A warp keeps its own running maximum, denominator
 // and 16 x 128 output, so nothing is exchanged while a unit lasts; the eight are joined in shared memory at its
 // end, and pieces of a unit that spans CTAs are joined by the CTA that finishes last, in block order.
@@ -20,10 +20,10 @@ namespace {
 
 constexpr int kD = 128;
 constexpr int kKeys = 64;
-constexpr int kUnits = 4;                    // unit descriptors in flight
+constexpr int kUnits = 3;                    // unit descriptors in flight
 constexpr int kHalf = kKeys * 128;           // [64 keys][64 columns] bf16
 constexpr int kStage = 4 * kHalf;            // per page: K lo, K hi, V lo, V hi of S rows; 32 KB in all
-constexpr int kStages = 4;
+constexpr int kStages = 6;
 // The two groups of consumers take alternate blocks, so a stage must always be the same group's: a warp may
 // only wait for a stage's next phase when it has waited for the one before (copies land out of order, and a
 // parity wait two phases ahead succeeds at once).
@@ -32,11 +32,11 @@ constexpr int kRows = kChunkFewRows;
 static_assert(kRows == 16, "one m16 tile");
 constexpr int kConsumers = 8;
 constexpr int kFewThreads = 32 * (kConsumers + 1);
-constexpr int kJoinF = 8 * kD;               // floats of a warp's join buffer: 8 rows
+constexpr int kJoinF = 4 * kD;               // floats of a warp's join buffer: 4 rows
 constexpr int kQRow = kD * 2 + 16;           // bytes of a query row in shared memory: rows 4 banks apart
 constexpr int kQBytes = kRows * kQRow;
 constexpr int kFewSmem = kStages * kStage + kConsumers * kJoinF * 4 + kUnits * kQBytes + 1024;
-static_assert(kFewSmem <= 220 * 1024, "shared memory");
+static_assert(kFewSmem <= 224 * 1024, "shared memory");
 static_assert(kChunkMaxRequests * 8 <= kStages * kStage, "the schedule's sums fit in the ring");
 constexpr float kRaise = 8.f;
 
@@ -73,7 +73,7 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
     pdl_trigger();
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float* join = reinterpret_cast<float*>(ring + kStages * kStage);  // [warp][8 rows][128]
+    float* join = reinterpret_cast<float*>(ring + kStages * kStage);  // [warp][4 rows][128]
     uint8_t* q_s = reinterpret_cast<uint8_t*>(join + kConsumers * kJoinF);  // [unit][16 rows][kQRow bytes]
     __shared__ __align__(8) uint64_t full[kStages], empty[kStages], u_full[kUnits], u_empty[kUnits];
     __shared__ UnitDesc unit_s[kUnits];
@@ -98,7 +98,7 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
     }
     pdl_wait();
     const ChunkShape sh{kRows / a.G, 0, kRows};
-    chunk_schedule<kKeys>(a, sh, 2, reinterpret_cast<long long*>(ring), red, &rg);
+    chunk_schedule<kKeys, 2>(a, sh, reinterpret_cast<long long*>(ring), red, &rg);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the ring held the schedule's sums
     __syncthreads();
 
@@ -324,45 +324,46 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
         const int tid = threadIdx.x;
         const size_t mine = (size_t)((int)blockIdx.x == p0 ? slot0 : 2 * blockIdx.x) * kRows;
 #pragma unroll 1
-        for (int half = 0; half < 2 && 8 * half < nrow; ++half) {
-            if (half) named_sync<32 * kConsumers>(1);  // the first eight rows have been read
-            if (half ? in1 : in0) {
-                // odd rows swap their float2 pairs, so that two rows' stores do not meet on the same banks
-                float* buf = join + warp * kJoinF + g4 * kD + 2 * (t4 ^ ((g4 & 1) << 1));
+        for (int pass = 0; 4 * pass < nrow; ++pass) {  // four rows at a time
+            if (pass) named_sync<32 * kConsumers>(1);  // the rows before have been read
+            if ((g4 >> 2) == (pass & 1) && (pass < 2 ? in0 : in1)) {
+                // groups of eight columns change places by row, so that four rows' stores use all banks
+                float* buf = join + warp * kJoinF + (g4 & 3) * kD + 2 * t4;
 #pragma unroll
                 for (int k = 0; k < 16; ++k)
-                    *reinterpret_cast<float2*>(buf + 8 * k) = half ? make_float2(o[k][2], o[k][3]) : make_float2(o[k][0], o[k][1]);
+                    *reinterpret_cast<float2*>(buf + 8 * (k ^ (g4 & 3))) =
+                        pass < 2 ? make_float2(o[k][0], o[k][1]) : make_float2(o[k][2], o[k][3]);
             }
             named_sync<32 * kConsumers>(1);
-            if (half == 0 && lane == 0) mbar_arrive(&u_empty[u % kUnits]);
-            const int r = 8 * half + warp;  // a warp per row, four columns per lane
+            if (pass == 0 && lane == 0) mbar_arrive(&u_empty[u % kUnits]);
+            const int rr = warp & 3, r = 4 * pass + rr;  // two warps per row, two columns per lane
             if (r < nrow) {
-                const int c = lane * 4;
+                const int c = (warp >> 2) * 64 + lane * 2;
+                const float* src = join + rr * kD + 8 * ((c >> 3) ^ rr) + (c & 7);
                 float M = -CUDART_INF_F, L = 0.f;
 #pragma unroll
                 for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, jm[w][r]);
                 const float mu = M == -CUDART_INF_F ? 0.f : M;
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                float2 v = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int w = 0; w < kConsumers; ++w) {
                     const float f = ex2f(jm[w][r] - mu);
-                    const float4 x = *reinterpret_cast<const float4*>(join + w * kJoinF + warp * kD + (c ^ ((warp & 1) << 2)));
+                    const float2 x = *reinterpret_cast<const float2*>(src + w * kJoinF);
                     L = fmaf(jl[w][r], f, L);
                     v.x = fmaf(x.x, f, v.x);
                     v.y = fmaf(x.y, f, v.y);
-                    v.z = fmaf(x.z, f, v.z);
-                    v.w = fmaf(x.w, f, v.w);
                 }
                 if (p0 < 0) {
                     const float inv = L > 0.f ? 1.f / L : 0.f;
-                    if (alive) store4<bf16>(out_ptr(r) + c, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+                    if (alive) *reinterpret_cast<uint32_t*>(out_ptr(r) + c) = pack_bf16(v.x * inv, v.y * inv);
                 } else {
-                    __stcg(reinterpret_cast<float4*>(a.part_o + (mine + r) * kD + c), v);
-                    if (lane == 0) __stcg(reinterpret_cast<float2*>(a.part_ml) + mine + r, make_float2(M, L));
+                    __stcg(reinterpret_cast<float2*>(a.part_o + (mine + r) * kD + c), v);
+                    if (warp < 4 && lane == 0) __stcg(reinterpret_cast<float2*>(a.part_ml) + mine + r, make_float2(M, L));
                 }
             }
         }
         if (p0 >= 0) {
+            // a unit shared with other CTAs: whoever arrives last adds the pieces in order, a warp per row
             __threadfence();
             named_sync<32 * kConsumers>(1);
             if (tid == 0)
@@ -370,25 +371,37 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
             named_sync<32 * kConsumers>(1);
             if (last_s) {
                 __threadfence();
-                auto piece = [&](int c) { return (size_t)(c == p0 ? slot0 : 2 * c) * kRows; };
-                for (int e = tid; e < nrow * 32; e += 32 * kConsumers) {
-                    const int r = e >> 5, c = (e & 31) * 4;
+                const int cnt = p1 - p0 + 1;
+                for (int r = warp; r < nrow; r += kConsumers) {
+                    auto at = [&](int k) { return (size_t)(k == 0 ? slot0 : 2 * (p0 + k)) * kRows + r; };
+                    const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
                     float M = -CUDART_INF_F;
-                    for (int k = p0; k <= p1; ++k) M = fmaxf(M, __ldcg(reinterpret_cast<const float2*>(a.part_ml) + piece(k) + r).x);
+                    for (int k = lane; k < cnt; k += 32) M = fmaxf(M, __ldcg(ml + at(k)).x);
+                    M = warp_max(M);
+                    const float mu = M == -CUDART_INF_F ? 0.f : M;
                     float L = 0.f;
                     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int k = p0; k <= p1 && M != -CUDART_INF_F; ++k) {
-                        const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + piece(k) + r);
-                        const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_o + (piece(k) + r) * kD + c));
-                        const float f = ex2f(ml.x - M);
-                        L = fmaf(ml.y, f, L);
-                        v.x = fmaf(x.x, f, v.x);
-                        v.y = fmaf(x.y, f, v.y);
-                        v.z = fmaf(x.z, f, v.z);
-                        v.w = fmaf(x.w, f, v.w);
+                    for (int k0 = 0; k0 < cnt; k0 += 32) {
+                        float f = 0.f;
+                        if (k0 + lane < cnt) {
+                            const float2 x = __ldcg(ml + at(k0 + lane));
+                            f = ex2f(x.x - mu);
+                            L = fmaf(x.y, f, L);
+                        }
+                        const int n_here = min(32, cnt - k0);
+#pragma unroll 4
+                        for (int k = 0; k < n_here; ++k) {
+                            const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_o + at(k0 + k) * kD + lane * 4));
+                            const float w = __shfl_sync(0xffffffffu, f, k);
+                            v.x = fmaf(x.x, w, v.x);
+                            v.y = fmaf(x.y, w, v.y);
+                            v.z = fmaf(x.z, w, v.z);
+                            v.w = fmaf(x.w, w, v.w);
+                        }
                     }
+                    L = warp_sum(L);
                     const float inv = L > 0.f ? 1.f / L : 0.f;
-                    if (alive) store4<bf16>(out_ptr(r) + c, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+                    if (alive) store4<bf16>(out_ptr(r) + lane * 4, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
                 }
             }
         }

@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_attn_simt_kernel(ChunkAttnD
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const ChunkShape sh{TR / a.G > 0 ? TR / a.G : 1, kTile ? kFew : 0, kTile ? 0x7fffffff : kFew};
-    chunk_schedule<KEYS>(a, sh, kTile ? 2 : 4, scr_raw, red, &rg);
+    chunk_schedule<KEYS, kTile ? 2 : 4>(a, sh, scr_raw, red, &rg);
     const float sl2 = a.scale * 1.4426950408889634f;
     const T* pool = reinterpret_cast<const T*>(a.kv_pool);
 

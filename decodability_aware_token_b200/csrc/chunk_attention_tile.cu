@@ -209,7 +209,7 @@ static_assert(32 * kSoftWarps * kSoftRegs + 128 * kIssueRegs <= kTileThreads * 1
 
 __global__ void __launch_bounds__(kTileThreads, 1)
 chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_constant__ CUtensorMap q_map,
-                       ChunkAttnDev a, int min_blocks) {
+                       ChunkAttnDev a) {
     pdl_trigger();
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* q_s = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -269,7 +269,7 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
 
     const int tpt = 128 / a.G;  // tokens per tile
     const ChunkShape sh{2 * tpt, a.G <= kChunkFewRows ? kChunkFewRows : 0, 0x7fffffff};
-    chunk_schedule<kKeys>(a, sh, min_blocks, reinterpret_cast<long long*>(k_ring), red, &rg);
+    chunk_schedule<kKeys, 4>(a, sh, reinterpret_cast<long long*>(k_ring), red, &rg);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the rings held the schedule's sums
     __syncthreads();
 
@@ -704,7 +704,7 @@ int launch_chunk_attention_tile(const ChunkAttnDev& a, int sms, cudaStream_t s) 
         pool_map = q_map;  // never used: without pages every key is invalid
     }
     const dim3 grid(sms < kChunkCtas ? sms : kChunkCtas), block(kTileThreads);
-    return launched(launch_pdl(chunk_attn_tile_kernel, grid, block, kSmem, s, 0, pool_map, q_map, a, 2));
+    return launched(launch_pdl(chunk_attn_tile_kernel, grid, block, kSmem, s, 0, pool_map, q_map, a));
 }
 
 }  // namespace focus

@@ -14,7 +14,7 @@
 namespace focus {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kAhead = 1;  // groups of heads whose loads are in flight while one is turned
 
 template <typename T, int V> struct Pack;  // 16 bytes
@@ -52,7 +52,7 @@ template <> struct Pack<float, 4> {
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 6) chunk_qk_kernel(ChunkQkDev a, int warps_per_row) {
+__global__ void __launch_bounds__(kThreads, 12) chunk_qk_kernel(ChunkQkDev a, int warps_per_row) {
     constexpr int V = 16 / (int)sizeof(T);      // values per access
     constexpr int LPH = D / 2 / V;              // lanes per head
     constexpr int HPW = 32 / LPH;               // heads a warp works on at once

@@ -69,6 +69,8 @@ struct ChunkRange {
     long long share;      // W / C
     int extra;            // W % C: CTAs 0 .. extra - 1 have share + 1 blocks
     int b, g, k, blk;     // where w0 lies
+    int tiles;            // tiles of request b
+    ChunkReq req;         // request b
 
     __device__ __forceinline__ long long start(int c) const { return share * c + min(c, extra); }
     // CTA whose range holds block w
@@ -78,15 +80,84 @@ struct ChunkRange {
     }
 };
 
+// The share of CTA blockIdx.x in a line of W blocks over at most gridDim.x CTAs of at least MINB blocks each.
+template <int MINB> __device__ __forceinline__ ChunkRange chunk_share(long long W) {
+    ChunkRange rg{};
+    if (W > 0) {
+        const long long want = chunk_div(W + MINB - 1, MINB);
+        const int C = (int)(want < gridDim.x ? want : (long long)gridDim.x), c = blockIdx.x;
+        rg.share = chunk_div(W, C);
+        rg.extra = (int)(W - rg.share * C);
+        if (c < C) {
+            rg.w0 = rg.start(c);
+            rg.w1 = rg.start(c + 1);
+        }
+    }
+    return rg;
+}
+
 // Fill *out (shared memory) for this CTA.  `scr` holds N long longs of shared memory, `red` 32.  Every thread of
-// the block calls it; it ends with a barrier.  min_blocks: smallest useful share of a CTA.
-template <int KEYS>
-__device__ void chunk_schedule(const ChunkAttnDev& a, const ChunkShape& sh, int min_blocks, long long* scr,
-                               long long* red, ChunkRange* out) {
+// the block calls it; it ends with a barrier.  MINB: smallest useful share of a CTA.
+template <int KEYS, int MINB>
+__device__ void chunk_schedule(const ChunkAttnDev& a, const ChunkShape& sh, long long* scr, long long* red,
+                               ChunkRange* out) {
     const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
-    // blocks of one KV head per request; requests of many tiles are left to whole warps
-    constexpr int kSerial = 4;
+    constexpr int kSerial = 4;  // tiles one thread counts by itself
     int any_long = 0;
+    if (a.N <= nt && a.small_walk) {
+        // a request per thread, sums in registers and 32 bits, three barriers; falls through if some request has
+        // many tiles
+        ChunkReq r{};
+        int tiles = 0;
+        uint32_t s = 0;
+        if (tid < a.N) {
+            r = chunk_req(a, tid, blockIdx.x == 0);
+            tiles = chunk_tiles(a, sh, r);
+            if (tiles > kSerial) any_long = 1;
+            else
+                for (int k = 0; k < tiles; ++k) s += (uint32_t)chunk_tile_blocks<KEYS>(r, a.mask_block, sh.tok, k);
+        }
+        uint32_t hi = s * a.Hkv;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t u = __shfl_up_sync(0xffffffffu, hi, o);
+            if (lane >= o) hi += u;
+        }
+        uint32_t* red32 = reinterpret_cast<uint32_t*>(red);
+        if (lane == 31) red32[warp] = hi;
+        if (!__syncthreads_or(any_long)) {
+            uint32_t before = 0, all = 0;
+#pragma unroll
+            for (int w = 0; w < 16; ++w) {
+                const uint32_t x = w < nw ? red32[w] : 0u;
+                if (w < warp) before += x;
+                all += x;
+            }
+            hi += before;
+            const uint32_t lo = hi - s * a.Hkv;
+            ChunkRange rg = chunk_share<MINB>(all);
+            const uint32_t w0 = (uint32_t)rg.w0;
+            if (rg.w0 < rg.w1 && hi > w0 && lo <= w0) {
+                rg.b = tid;
+                rg.g = (int)((w0 - lo) / s);
+                rg.req = r;
+                rg.tiles = tiles;
+                int rem = (int)(w0 - lo - (uint32_t)rg.g * s);
+                for (;; ++rg.k) {
+                    const int nb = chunk_tile_blocks<KEYS>(r, a.mask_block, sh.tok, rg.k);
+                    if (rem < nb) break;
+                    rem -= nb;
+                }
+                rg.blk = rem;
+                *out = rg;
+            } else if (rg.w0 >= rg.w1 && tid == 0) {
+                *out = rg;
+            }
+            __syncthreads();
+            return;
+        }
+    }
+    // blocks of one KV head per request; requests of many tiles are left to whole warps
     for (int b = tid; b < a.N; b += nt) {
         const ChunkReq r = chunk_req(a, b, blockIdx.x == 0);
         const int tiles = chunk_tiles(a, sh, r);
@@ -136,18 +207,7 @@ __device__ void chunk_schedule(const ChunkAttnDev& a, const ChunkShape& sh, int 
         __syncthreads();
     }
     const long long W = carry;
-    const int c = blockIdx.x;
-    ChunkRange rg{};
-    if (W > 0) {
-        const long long want = chunk_div(W + min_blocks - 1, min_blocks);
-        const int C = (int)(want < gridDim.x ? want : (long long)gridDim.x);
-        rg.share = chunk_div(W, C);
-        rg.extra = (int)(W - rg.share * C);
-        if (c < C) {
-            rg.w0 = rg.start(c);
-            rg.w1 = rg.start(c + 1);
-        }
-    }
+    const ChunkRange rg = chunk_share<MINB>(W);
     if (tid == 0) *out = rg;
     __syncthreads();
     if (rg.w0 < rg.w1) {  // (the same in every thread)
@@ -161,12 +221,13 @@ __device__ void chunk_schedule(const ChunkAttnDev& a, const ChunkShape& sh, int 
             out->g = g;
             out->k = 0;
             out->blk = (int)(off - g * per);  // (more than an int holds only with many tiles, found below)
-            if (chunk_tiles(a, sh, chunk_req(a, b, false)) > 1) many = 1;
+            out->req = chunk_req(a, b, false);
+            out->tiles = chunk_tiles(a, sh, out->req);
+            if (out->tiles > 1) many = 1;
         }
         if (__syncthreads_or(many) && warp == 0) {
-            const int b = out->b, g = out->g;
-            const ChunkReq r = chunk_req(a, b, false);
-            const int tiles = chunk_tiles(a, sh, r);
+            const int b = out->b, g = out->g, tiles = out->tiles;
+            const ChunkReq r = out->req;
             const long long lo = b ? scr[b - 1] : 0;
             long long rem = rg.w0 - lo - g * chunk_div(scr[b] - lo, a.Hkv);
             for (int k0 = 0; k0 < tiles; k0 += 32) {
@@ -209,8 +270,8 @@ struct ChunkWalk {
         k = rg.k;
         blk0 = rg.blk;
         if (w < w1) {
-            r = chunk_req(a, b, false);
-            tiles = chunk_tiles(a, sh, r);
+            r = rg.req;
+            tiles = rg.tiles;
             fit(a, sh);
         }
     }
