@@ -2,12 +2,14 @@
 // speculative ones) over the paged cache, on mma.sync m16n8k16: with 16 rows the tensor work is a fraction of the
 // copy time whatever the instruction, and fragments in registers need no TMEM round trip per block.
 //
-// Bound by memory: each cached key and value is read once (64 Hkv d bytes ... per 16-key step 8 KB), so the design
-// is a copy that never stops.  One CTA per SM walks its equal share of the batch's key blocks (chunk_work.cuh);
-// one warp issues the pages of 64-key blocks by TMA into a ring of six 32 KB stages and runs on across unit
-// ends; eight warps consume, four per block, 16 keys each.  A warp keeps its own running maximum, denominator
-// and 16 x 128 output, so nothing is exchanged while a unit lasts; the eight are joined in shared memory at its
-// end, and pieces of a unit that spans CTAs are joined by the CTA that finishes last, in block order.
+// Bound by memory: each cached key and value is read once, so the design is a copy that never stops.  One CTA
+// per SM walks its equal share of the batch's key blocks (chunk_work.cuh); one warp issues the pages of 64-key
+// blocks by TMA into a ring of six 32 KB stages and runs on across unit ends.  Two groups of four warps consume
+// alternate units, 16 keys of a block per warp: a group keeps up with the copies (600 to 700 ns a block of
+// compute against 740 at the copy rate), and while it joins its warps' results and writes them, the other one
+// is already at the next unit.  A warp keeps its own running maximum, denominator and 16 x 128 output, so
+// nothing is exchanged while a unit lasts.  Pieces of a unit that spans CTAs are joined by the CTA that finishes
+// last, in block order.
 //
 // Weights are rounded to bf16 for the product with V (relative 2^-9 each, as the values' own type); maxima,
 // denominators and outputs are float32.  The running maximum is raised only by more than 2^8.
@@ -20,19 +22,17 @@ namespace {
 
 constexpr int kD = 128;
 constexpr int kKeys = 64;
-constexpr int kUnits = 3;                    // unit descriptors in flight
+constexpr int kUnits = 4;                    // unit descriptors in flight
 constexpr int kHalf = kKeys * 128;           // [64 keys][64 columns] bf16
 constexpr int kStage = 4 * kHalf;            // per page: K lo, K hi, V lo, V hi of S rows; 32 KB in all
 constexpr int kStages = 6;
-// The two groups of consumers take alternate blocks, so a stage must always be the same group's: a warp may
-// only wait for a stage's next phase when it has waited for the one before (copies land out of order, and a
-// parity wait two phases ahead succeeds at once).
-static_assert(kStages % 2 == 0, "a stage belongs to one group of consumers");
 constexpr int kRows = kChunkFewRows;
 static_assert(kRows == 16, "one m16 tile");
 constexpr int kConsumers = 8;
+constexpr int kGroup = 4;                    // warps that consume a unit
+static_assert(kUnits % 2 == 0, "a descriptor slot belongs to one group: its waits see every phase");
 constexpr int kFewThreads = 32 * (kConsumers + 1);
-constexpr int kJoinF = 4 * kD;               // floats of a warp's join buffer: 4 rows
+constexpr int kJoinF = 2 * kD;               // floats of a warp's join buffer: 2 rows
 constexpr int kQRow = kD * 2 + 16;           // bytes of a query row in shared memory: rows 4 banks apart
 constexpr int kQBytes = kRows * kQRow;
 constexpr int kFewSmem = kStages * kStage + kConsumers * kJoinF * 4 + kUnits * kQBytes + 1024;
@@ -73,25 +73,28 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
     pdl_trigger();
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float* join = reinterpret_cast<float*>(ring + kStages * kStage);  // [warp][4 rows][128]
+    float* join = reinterpret_cast<float*>(ring + kStages * kStage);  // [warp][2 rows][128]
     uint8_t* q_s = reinterpret_cast<uint8_t*>(join + kConsumers * kJoinF);  // [unit][16 rows][kQRow bytes]
     __shared__ __align__(8) uint64_t full[kStages], empty[kStages], u_full[kUnits], u_empty[kUnits];
     __shared__ UnitDesc unit_s[kUnits];
     __shared__ uint32_t bad_s[kStages];       // 16-key groups of the stage whose page id is invalid
+    __shared__ volatile uint32_t tag_s[kStages];  // block the stage is being filled with
+    __shared__ uint32_t first_s[kUnits];      // number of the unit's first block in the CTA's walk
     __shared__ ChunkRange rg;
     __shared__ long long red[32];
     __shared__ float jm[kConsumers][kRows], jl[kConsumers][kRows];
-    __shared__ int last_s;
+    __shared__ int last_s[2];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 4);  // the four warps that consume the block
+            mbar_init(&empty[s], kGroup);
+            tag_s[s] = ~0u;
         }
         for (int s = 0; s < kUnits; ++s) {
             mbar_init(&u_full[s], 1);
-            mbar_init(&u_empty[s], kConsumers);
+            mbar_init(&u_empty[s], kGroup);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&pool_map) : "memory");
@@ -116,6 +119,7 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
             const int nrow = live ? min(sh.tok, wk.r.n - wk.k * sh.tok) * a.G : 0;
             if (lane == 0) {
                 describe(unit_s[s], wk, rg, sh, live);
+                first_s[s] = n;
                 mbar_expect_tx(&u_full[s], (uint32_t)nrow * 256u);
             }
             __syncwarp();
@@ -149,6 +153,7 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
                 if (el) {
                     if (bad) raise_err(a.err, FOCUS_DEVERR_PAGE_ID);
                     bad_s[st] = bad;
+                    tag_s[st] = n;
                     mbar_expect_tx(&full[st], (uint32_t)(good * a.S) * 512u);
                 }
                 __syncwarp();
@@ -161,28 +166,48 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
                 __syncwarp();
             }
         }
-        if (ok) publish(false);
+        if (ok && publish(false)) publish(false);  // an end for each group
         // never leave with copies in flight
         for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i) warp_wait(&full[i % kStages], (i / kStages) & 1u, a.err);
         for (uint32_t i = d > kUnits ? d - kUnits : 0; i < d; ++i) warp_wait(&u_full[i % kUnits], (i / kUnits) & 1u, a.err);
         return;
     }
 
-    // ---- consumers: warps 0-3 take the even blocks of the CTA's walk, 4-7 the odd ones
-    const int grp = warp >> 2, ks = (warp & 3) * 16;  // this warp's 16 keys of a block
+    // ---- consumers: warps 0-3 take the even units of the CTA's walk, 4-7 the odd ones
+    const int grp = warp / kGroup, wq = warp % kGroup, ks = wq * 16;  // this warp's 16 keys of a block
     const int g4 = lane >> 2, t4 = lane & 3;          // fragment row, column pair
     const float sl2 = a.scale * 1.4426950408889634f;
+    // row / G for rows below 16
+    const uint32_t g_inv = (65536u + a.G - 1) / a.G;
+    auto token = [&](int r) { return (int)(((uint32_t)r * g_inv) >> 16); };
+    const int tk0 = token(g4), tk1 = token(g4 + 8);
     // ldmatrix row addresses within a stage: K (keys x 32 columns a step), V transposed (16 keys x 16 columns)
     // (the warp's 16 keys lie in one page: S is a multiple of 16)
     const uint32_t key_off = (uint32_t)(ks / a.S * a.S * 512 + ks % a.S * 128), half_off = (uint32_t)a.S * 128u;
     const int krow = lane & 7, kc = lane >> 3;                      // + 8 keys per n tile, 16-byte column kc
     const int vrow = (lane & 7) + ((lane >> 3) & 1) * 8, vc = lane >> 4;
-    uint32_t n = 0;
     bool alive = true;
-    for (uint32_t u = 0;; ++u) {
-        // the eight warps go on or stop together: a wait that gave up in one of them alone would leave the others
+    // Block n has landed in its stage.  The stage's earlier blocks may have been the other group's, so first wait
+    // until it is being filled with block n: the earlier phases are over then, and the parity is unambiguous.
+    auto block_here = [&](uint32_t n) {
+        const uint32_t st = n % kStages;
+        bool seen = tag_s[st] == n;
+        if (!seen) {
+            const long long t0 = clock64();
+            while (!(seen = tag_s[st] == n)) {
+                if (clock64() - t0 > tc::kWaitCycles) {
+                    raise_err(a.err, FOCUS_DEVERR_TIMEOUT);
+                    break;
+                }
+                __nanosleep(20);  // (a group waits here while the other one is at its unit)
+            }
+        }
+        return __all_sync(0xffffffffu, seen) && warp_wait(&full[st], (n / kStages) & 1u, a.err);
+    };
+    for (uint32_t u = grp;; u += 2) {
+        // the group's warps go on or stop together: a wait that gave up in one of them alone would leave the others
         // at a named barrier
-        if (!all_agree<32 * kConsumers>(1, warp_wait(&u_full[u % kUnits], (u / kUnits) & 1u, a.err))) break;
+        if (!all_agree<32 * kGroup>(1 + grp, warp_wait(&u_full[u % kUnits], (u / kUnits) & 1u, a.err))) break;
         const UnitDesc& ud = unit_s[u % kUnits];
         const int nb = ud.nb;
         if (nb == 0) break;
@@ -199,8 +224,8 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
             q[s][2] = in0 ? *reinterpret_cast<const uint32_t*>(qr + 32 * s + 16) : 0u;
             q[s][3] = in1 ? *reinterpret_cast<const uint32_t*>(qr + 8 * kQRow + 32 * s + 16) : 0u;
         }
-        const int lim0 = in0 ? chunk_visible(pos0 + g4 / a.G, kv, a.mask_block) : 0;
-        const int lim1 = in1 ? chunk_visible(pos0 + (g4 + 8) / a.G, kv, a.mask_block) : 0;
+        const int lim0 = in0 ? chunk_visible(pos0 + tk0, kv, a.mask_block) : 0;
+        const int lim1 = in1 ? chunk_visible(pos0 + tk1, kv, a.mask_block) : 0;
         const int lim_all = chunk_visible(pos0, kv, a.mask_block);  // the fewest keys a row sees
         float m0 = -CUDART_INF_F, m1 = -CUDART_INF_F, l0 = 0.f, l1 = 0.f;
         float o[16][4];
@@ -209,21 +234,21 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
 #pragma unroll
             for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
 
+        uint32_t n = first_s[u % kUnits];
         for (int i = 0; i < nb; ++i, ++n) {
-            if ((int)(n & 1u) != grp) continue;
             const uint32_t st = n % kStages;
-            alive = alive && warp_wait(&full[st], (n / kStages) & 1u, a.err);
+            alive = alive && block_here(n);
             if (!alive) continue;
             const int key0 = (ud.blk0 + i) * kKeys + ks;
             const uint32_t bad = (bad_s[st] >> (ks >> 4)) & 1u;
             uint8_t* stage = ring + st * kStage;
             const uint32_t kb = smem_u32(stage) + key_off, vb = kb + 2 * half_off;
-            float s[2][4];
+            // S: 16 rows x 16 keys, 128 columns; even and odd steps of 16 columns in chains of their own
+            float s[2][4], s_odd[2][4];
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
-            // S: 16 rows x 16 keys, 128 columns
+                for (int e = 0; e < 4; ++e) s[j][e] = s_odd[j][e] = 0.f;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {  // 32 columns: 16-byte chunks 4 c .. 4 c + 3 of 16
                 const int ch = 4 * (c & 1) + kc;
@@ -233,9 +258,13 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
                     uint32_t b[4];
                     ldsm4(b, kb + (c >> 1) * half_off + row * 128 + ((ch ^ (row & 7)) << 4));
                     mma16816(s[j], q[2 * c], b[0], b[1]);
-                    mma16816(s[j], q[2 * c + 1], b[2], b[3]);
+                    mma16816(s_odd[j], q[2 * c + 1], b[2], b[3]);
                 }
             }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[j][e] += s_odd[j][e];
             if (key0 + 16 > lim_all || bad) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
@@ -304,7 +333,7 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[st]);
         }
-        // ---- join the eight warps: maxima and denominators, then the outputs, eight rows at a time, in warp order
+        // ---- join the group's warps: maxima and denominators, then the outputs, two rows at a time, in warp order
 #pragma unroll
         for (int w = 1; w < 4; w <<= 1) {
             l0 += __shfl_xor_sync(0xffffffffu, l0, w);
@@ -319,37 +348,37 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
         const int row0 = ud.row0, tok0 = ud.tok0, g = ud.g, p0 = ud.c0, p1 = ud.c1, slot0 = ud.slot0;
         bf16* out = reinterpret_cast<bf16*>(a.out);
         auto out_ptr = [&](int r) {
-            return out + (long long)(row0 + tok0 + r / a.G) * a.out_stride + (g * a.G + r % a.G) * kD;
+            return out + (long long)(row0 + tok0 + token(r)) * a.out_stride + (g * a.G + r - token(r) * a.G) * kD;
         };
-        const int tid = threadIdx.x;
         const size_t mine = (size_t)((int)blockIdx.x == p0 ? slot0 : 2 * blockIdx.x) * kRows;
+        auto sync = [&]() { named_sync<32 * kGroup>(1 + grp); };
 #pragma unroll 1
-        for (int pass = 0; 4 * pass < nrow; ++pass) {  // four rows at a time
-            if (pass) named_sync<32 * kConsumers>(1);  // the rows before have been read
-            if ((g4 >> 2) == (pass & 1) && (pass < 2 ? in0 : in1)) {
-                // groups of eight columns change places by row, so that four rows' stores use all banks
-                float* buf = join + warp * kJoinF + (g4 & 3) * kD + 2 * t4;
+        for (int pass = 0; 2 * pass < nrow; ++pass) {
+            if (pass) sync();  // the rows before have been read (pass 0: by the barrier at the unit's start)
+            if ((g4 >> 1) == (pass & 3) && (pass < 4 ? in0 : in1)) {
+                // groups of eight columns change places by row, so that both rows' stores use all banks
+                float* buf = join + warp * kJoinF + (g4 & 1) * kD + 2 * t4;
 #pragma unroll
                 for (int k = 0; k < 16; ++k)
-                    *reinterpret_cast<float2*>(buf + 8 * (k ^ (g4 & 3))) =
-                        pass < 2 ? make_float2(o[k][0], o[k][1]) : make_float2(o[k][2], o[k][3]);
+                    *reinterpret_cast<float2*>(buf + 8 * (k ^ (g4 & 1))) =
+                        pass < 4 ? make_float2(o[k][0], o[k][1]) : make_float2(o[k][2], o[k][3]);
             }
-            named_sync<32 * kConsumers>(1);
+            sync();
             if (pass == 0 && lane == 0) mbar_arrive(&u_empty[u % kUnits]);
-            const int rr = warp & 3, r = 4 * pass + rr;  // two warps per row, two columns per lane
+            const int rr = wq & 1, r = 2 * pass + rr;  // two warps per row, two columns per lane
             if (r < nrow) {
-                const int c = (warp >> 2) * 64 + lane * 2;
-                const float* src = join + rr * kD + 8 * ((c >> 3) ^ rr) + (c & 7);
+                const int c = (wq >> 1) * 64 + lane * 2;
+                const float* src = join + grp * kGroup * kJoinF + rr * kD + 8 * ((c >> 3) ^ rr) + (c & 7);
                 float M = -CUDART_INF_F, L = 0.f;
 #pragma unroll
-                for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, jm[w][r]);
+                for (int w = 0; w < kGroup; ++w) M = fmaxf(M, jm[grp * kGroup + w][r]);
                 const float mu = M == -CUDART_INF_F ? 0.f : M;
                 float2 v = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int w = 0; w < kConsumers; ++w) {
-                    const float f = ex2f(jm[w][r] - mu);
+                for (int w = 0; w < kGroup; ++w) {
+                    const float f = ex2f(jm[grp * kGroup + w][r] - mu);
                     const float2 x = *reinterpret_cast<const float2*>(src + w * kJoinF);
-                    L = fmaf(jl[w][r], f, L);
+                    L = fmaf(jl[grp * kGroup + w][r], f, L);
                     v.x = fmaf(x.x, f, v.x);
                     v.y = fmaf(x.y, f, v.y);
                 }
@@ -358,21 +387,22 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
                     if (alive) *reinterpret_cast<uint32_t*>(out_ptr(r) + c) = pack_bf16(v.x * inv, v.y * inv);
                 } else {
                     __stcg(reinterpret_cast<float2*>(a.part_o + (mine + r) * kD + c), v);
-                    if (warp < 4 && lane == 0) __stcg(reinterpret_cast<float2*>(a.part_ml) + mine + r, make_float2(M, L));
+                    if (wq < 2 && lane == 0) __stcg(reinterpret_cast<float2*>(a.part_ml) + mine + r, make_float2(M, L));
                 }
             }
         }
         if (p0 >= 0) {
             // a unit shared with other CTAs: whoever arrives last adds the pieces in order, a warp per row
             __threadfence();
-            named_sync<32 * kConsumers>(1);
-            if (tid == 0)
-                last_s = atomicInc(reinterpret_cast<unsigned*>(a.counters) + p0, (unsigned)(p1 - p0)) == (unsigned)(p1 - p0);
-            named_sync<32 * kConsumers>(1);
-            if (last_s) {
+            sync();
+            if (wq == 0 && lane == 0)
+                last_s[grp] = atomicInc(reinterpret_cast<unsigned*>(a.counters) + p0, (unsigned)(p1 - p0)) ==
+                              (unsigned)(p1 - p0);
+            sync();
+            if (last_s[grp]) {
                 __threadfence();
                 const int cnt = p1 - p0 + 1;
-                for (int r = warp; r < nrow; r += kConsumers) {
+                for (int r = wq; r < nrow; r += kGroup) {
                     auto at = [&](int k) { return (size_t)(k == 0 ? slot0 : 2 * (p0 + k)) * kRows + r; };
                     const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
                     float M = -CUDART_INF_F;
@@ -405,7 +435,6 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
                 }
             }
         }
-        named_sync<32 * kConsumers>(1);  // the join buffers are free for the next unit
     }
 }
 
