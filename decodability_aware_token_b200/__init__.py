@@ -224,6 +224,48 @@ class FocusContext:
                                                 C.byref(steps), C.c_void_p(s.cuda_stream)), "focus_decode_block")
         return out, int(steps.value)
 
+    def prefill(self, chunk: "ChunkContext", tokens: torch.Tensor, new_len: torch.Tensor, batch: dict,
+                free_pages: torch.Tensor, free_head: torch.Tensor, *, max_rows: Optional[int] = None, mask_block: int = 1,
+                q_norm=None, k_norm=None, hidden: Optional[torch.Tensor] = None, out: Optional["ChunkPlan"] = None,
+                stream: Optional[torch.cuda.Stream] = None) -> "ChunkPlan":
+        """Run a chunk of prompt tokens through the model (focus_prefill): its keys and values go into pages taken
+        from free_pages[free_head ...], batch["page_table"] and batch["prefix_len"] are updated in place.
+
+        tokens [N, max_new] int32, new_len [N] int32; `batch` holds prefix_len, page_table and kv_pool as for a
+        step; `chunk` is a ChunkContext of this model's geometry.  `max_rows` (or `out`) bounds the rows, at most
+        max_requests * max_block of this context.  q_norm / k_norm: optional lists of L gains [d].  `hidden`
+        [max_rows, D] float32 receives the last layer's residual rows.  Asynchronous."""
+        if out is None and max_rows is None:
+            max_rows = min(tokens.numel(), self.limits.max_requests * self.limits.max_block)
+        pool = batch["kv_pool"]
+        n_pages, page_size, pool_ptr = chunk._pool(pool, 0)
+        packed, out = chunk._plan_args(batch["prefix_len"], new_len, batch["page_table"], free_pages, free_head, page_size,
+                                       n_pages, max_rows, out)
+        plan = _abi.ChunkPlanArgs.from_buffer_copy(packed)
+        if tokens.dim() != 2 or tokens.shape[0] != plan.n_requests:
+            raise ValueError(f"tokens: shape {tuple(tokens.shape)}, expected [{plan.n_requests}, max_new]")
+        _need(tokens, "tokens", torch.int32, self.device)
+        if chunk.device != self.device:
+            raise ValueError(f"chunk: on {chunk.device}, expected {self.device}")
+        if hidden is not None:
+            _need(hidden, "hidden", torch.float32, self.device, (plan.max_rows, self.shape.hidden))
+        gains = []
+        for name, ts in (("q_norm", q_norm), ("k_norm", k_norm)):
+            if ts is None:
+                gains.append(None)
+                continue
+            if len(ts) != self.shape.n_layers:
+                raise ValueError(f"{name}: expected {self.shape.n_layers} layers")
+            for l, t in enumerate(ts):
+                _need(t, f"{name}[{l}]", self.dtype, self.device, (self.shape.head_dim,))
+            gains.append((C.c_void_p * len(ts))(*[t.data_ptr() for t in ts]))
+        args = _abi.PrefillArgs(C.pointer(plan), _ptr(tokens), max(1, tokens.shape[1]), mask_block, pool_ptr,
+                                *[C.cast(g, C.POINTER(C.c_void_p)) if g is not None else None for g in gains], _ptr(hidden))
+        with torch.cuda.device(self.device):
+            s = stream if stream is not None else torch.cuda.current_stream(self.device)
+            _check(self._lib.focus_prefill(self._ctx, chunk._ctx, C.byref(args), C.c_void_p(s.cuda_stream)), "focus_prefill")
+        return out
+
     def probe_wait_timeout(self, stream: Optional[torch.cuda.Stream] = None) -> None:
         """Enqueue the failure-path probe: a bounded pipeline wait that nothing satisfies gives up after
         about a second and flags FOCUS_DEVERR_TIMEOUT (read it with device_error)."""

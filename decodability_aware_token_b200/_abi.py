@@ -29,7 +29,7 @@ EXPORTED = ("focus_init", "focus_step", "focus_destroy", "focus_status_string", 
             "focus_workspace_bytes", "focus_last_step_launches", "focus_profile_begin", "focus_profile_end",
             "focus_lm_head_conf_noalloc", "focus_commit_block", "focus_decode_block", "focus_probe_wait_timeout",
             "focus_chunk_init", "focus_chunk_destroy", "focus_chunk_workspace_bytes", "focus_chunk_get_device_error",
-            "focus_chunk_plan_rows", "focus_chunk_qk_norm_rope", "focus_chunk_attention")
+            "focus_chunk_plan_rows", "focus_chunk_qk_norm_rope", "focus_chunk_attention", "focus_prefill")
 
 KERNEL_CLASSES = ("embed_norm", "qkv_finalize", "attn_score", "attn_ragged", "row_norm", "select", "decode",
                   "gemm_full_qkv", "gemm_full_o", "gemm_full_gateup", "gemm_full_down",
@@ -104,7 +104,13 @@ class ChunkAttnArgs(C.Structure):
                 ("row_offsets", C.c_void_p), ("kv_len", C.c_void_p), ("page_table", C.c_void_p), ("out", C.c_void_p)]
 
 
-# The same three argument structs as packed bytes (native alignment): a call builds one bytes object instead of
+class PrefillArgs(C.Structure):
+    _fields_ = [("plan", C.POINTER(ChunkPlanArgs)), ("tokens", C.c_void_p), ("max_new", C.c_int32),
+                ("mask_block", C.c_int32), ("kv_pool", C.c_void_p), ("q_norm", C.POINTER(C.c_void_p)),
+                ("k_norm", C.POINTER(C.c_void_p)), ("hidden", C.c_void_p)]
+
+
+# The chunk operators' argument structs as packed bytes (native alignment): a call builds one bytes object instead of
 # setting a field at a time, which costs more host time than a small kernel takes.
 PLAN_PACK = struct.Struct("@5i11P")
 QK_PACK = struct.Struct("@4if4q9P")
@@ -179,5 +185,7 @@ def load():
     lib.focus_chunk_qk_norm_rope.restype = C.c_int
     lib.focus_chunk_attention.argtypes = [C.c_void_p, C.POINTER(ChunkAttnArgs), C.c_void_p]
     lib.focus_chunk_attention.restype = C.c_int
+    lib.focus_prefill.argtypes = [C.c_void_p, C.c_void_p, C.POINTER(PrefillArgs), C.c_void_p]
+    lib.focus_prefill.restype = C.c_int
     _lib = lib
     return lib

@@ -145,6 +145,11 @@ class ChunkContext:
         prefix_len, new_len [N] int32; page_table [N, max_pages_per_req] int32, new pages are written into it;
         free_pages [F] int32, taken from index free_head [1] int32 on.  `max_rows` (or the size of `out`)
         bounds the rows.  A request that does not fit gets no rows: row_offsets tells."""
+        args, out = self._plan_args(prefix_len, new_len, page_table, free_pages, free_head, page_size, n_pages, max_rows, out)
+        self._call(0, args, "focus_chunk_plan_rows", stream)
+        return out
+
+    def _plan_args(self, prefix_len, new_len, page_table, free_pages, free_head, page_size, n_pages, max_rows, out):
         n = prefix_len.shape[0]
         if out is None:
             if max_rows is None:
@@ -154,14 +159,12 @@ class ChunkContext:
         if max_rows is not None and max_rows != rows:
             raise ValueError(f"plan: out holds {rows} rows, max_rows is {max_rows}")
         i, per_req, per_row, n_free = self._ints, (n,), (rows,), free_pages.shape[0]
-        args = _abi.PLAN_PACK.pack(
+        return _abi.PLAN_PACK.pack(
             n, rows, page_size, n_pages, n_free, i(prefix_len, "prefix_len", per_req), i(new_len, "new_len", per_req),
             i(page_table, "page_table", (n, self.limits.max_pages_per_req)), i(free_pages, "free_pages", (n_free,)),
             i(free_head, "free_head", (1,)), i(out.row_offsets, "row_offsets", (n + 1,)), i(out.kv_len, "kv_len", per_req),
             i(out.row_req, "row_req", per_row), i(out.row_pos, "row_pos", per_row), i(out.row_slot, "row_slot", per_row),
-            i(out.free_next, "free_next", (1,)))
-        self._call(0, args, "focus_chunk_plan_rows", stream)
-        return out
+            i(out.free_next, "free_next", (1,))), out
 
     def qk_norm_rope(self, q, k, v, kv_pool, layer: int, row_pos, row_slot, *, q_norm=None, k_norm=None,
                      eps: float = 1e-6, out: Optional[torch.Tensor] = None,

@@ -22,6 +22,8 @@ struct focus_chunk_ctx {
     int* counters;
 };
 
+const focus_chunk_cfg* focus::chunk_cfg(const focus_chunk_ctx* c) { return &c->cfg; }
+
 namespace {
 
 bool cfg_ok(const focus_chunk_cfg* c) {

@@ -197,12 +197,37 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(ChunkPlanDev a) {
     }
 }
 
+__global__ void __launch_bounds__(kThreads) chunk_tokens_kernel(focus_chunk_plan p, const int32_t* __restrict__ tokens,
+                                                                int max_new, int32_t* __restrict__ out, int* err) {
+    pdl_entry();
+    const int i = blockIdx.x * kThreads + threadIdx.x;
+    if (i < p.max_rows) {
+        const int b = p.row_req[i];
+        int tok = 0;
+        if (b >= 0) {
+            const int at = i - p.row_offsets[b];
+            if (at < max_new) tok = tokens[(size_t)b * max_new + at];
+            else raise_err(err, FOCUS_DEVERR_ROWS);
+        }
+        out[i] = tok;
+    }
+    if (i < p.n_requests) const_cast<int32_t*>(p.prefix_len)[i] = p.kv_len[i];
+}
+
 }  // namespace
+
+int launch_chunk_tokens(const focus_chunk_plan& p, const int32_t* tokens, int max_new, int32_t* out, int* err,
+                        cudaStream_t s) {
+    const int n = p.max_rows > p.n_requests ? p.max_rows : p.n_requests;
+    return launched(launch_pdl(chunk_tokens_kernel, dim3((n + kThreads - 1) / kThreads), dim3(kThreads), 0, s, 0, p, tokens,
+                               max_new, out, err));
+}
 
 bool configure_chunk_plan_kernel() {
     return cudaFuncSetAttribute(chunk_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (3 * kChunkMaxRequests + 1) * 4) == cudaSuccess &&
-           max_shared_carveout((const void*)chunk_plan_kernel);
+           max_shared_carveout((const void*)chunk_plan_kernel) &&
+           max_shared_carveout((const void*)chunk_tokens_kernel);
 }
 
 int launch_chunk_plan(const ChunkPlanDev& a, cudaStream_t s) {

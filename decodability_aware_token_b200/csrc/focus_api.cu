@@ -19,6 +19,7 @@
 #include "launch.h"
 #include "tc_gemm.h"
 #include "block.h"
+#include "chunk.h"
 
 using namespace focus;
 
@@ -41,6 +42,7 @@ struct focus_ctx {
     double* inv_freq;
     float2* rope_tab;     // bf16 path: [rope_positions][head_dim / 2] (cos, sin)
     int32_t* masked_count;  // block loop: masked positions left after a step
+    int32_t* zeros;         // [max_requests * max_block] zeros: prefix lengths of rows that are not rotated (prefill)
     int32_t* req_order;     // [max_requests] requests by descending prefix length (kept-row attention order)
     int* err;
     float *att_part_o, *att_part_ml, *att_sb;
@@ -141,10 +143,11 @@ Layout plan(const focus_model_cfg* c, const focus_limits* l) {
         split * rope_positions(l) * (size_t)c->head_dim / 2 * 8,  // 23 RoPE (cos, sin) table
         64,                                                 // 24 block loop: masked-position count
         (size_t)l->max_requests * 4,                        // 25 request order
+        rows_full * 4,                                      // 26 zeros
     };
     Layout lay{};
     size_t at = 0;
-    for (int i = 0; i < 26; ++i) {
+    for (int i = 0; i < 27; ++i) {
         lay.off[i] = at;
         at = align_up(at + sizes[i], 1024);
     }
@@ -363,6 +366,71 @@ int run_step(focus_ctx* c, const focus_batch* in, const focus_params* p, focus_s
     return FOCUS_OK;
 }
 
+// A chunk of prompt tokens through the model (focus_prefill): the chunk operators between the step's own GEMMs and
+// row kernels.  The QKV projection's rows have to arrive unrotated: the tensor-core epilogue is given position 0 of
+// every row (a turn by 0, exact) and rows as blocks of one position, so that it leaves the queries in c->q and
+// keys and values side by side in c->part; the CUDA-core GEMM leaves the float32 row there as a whole.
+template <typename T>
+int run_prefill(focus_ctx* c, focus_chunk_ctx* k, const focus_prefill_args* p, cudaStream_t s) {
+    const Dims& dm = c->dm;
+    const focus_chunk_plan& pl = *p->plan;
+    const int T_rows = pl.max_rows;
+    const bool tc = c->cfg.dtype == FOCUS_DTYPE_BF16;
+    const size_t stride = c->split_stride, hd = (size_t)dm.Hq * dm.d, kvd = (size_t)dm.Hkv * dm.d;
+    T* h = reinterpret_cast<T*>(c->h);
+    auto W = [](const void* ptr) { return reinterpret_cast<const T*>(ptr); };
+    int rc = focus_chunk_plan_rows(k, &pl, s);
+    if (rc != FOCUS_OK || T_rows == 0) return rc;
+    int32_t* tok = reinterpret_cast<int32_t*>(c->act);  // read before the first MLP writes there
+    bool bad = launch_chunk_tokens(pl, p->tokens, p->max_new, tok, c->err, s) < 0;
+    bad = launch_embed_norm<T>(tok, T_rows, dm.V, W(c->embed), W(c->attn_norm[0]), dm.eps, dm.D, c->x_full, h, c->err, s) < 0 || bad;
+    auto gemm = [&](Epi epi, const void* A, const void* Bw, const void* B2, int Nn, int K, float* resid) {
+        GemmArgs g{};
+        g.A = A; g.B = Bw; g.B2 = B2; g.M_bound = T_rows; g.N = Nn; g.K = K; g.splits = 1;
+        g.part = c->part; g.split_stride = stride; g.act = c->act; g.resid = resid;
+        g.q_out = c->q; g.ibc = c->part; g.prefix_len = c->zeros; g.inv_freq = c->inv_freq; g.rope_tab = c->rope_tab;
+        g.max_prefix = 0; g.block = 1; g.n_layers = 1; g.layer = 0; g.Hq = dm.Hq; g.Hkv = dm.Hkv; g.err = c->err;
+        if (tc) return tc_gemm(c->tc, epi, g, s);
+        g.n_tiles = (Nn + kSimtTileN - 1) / kSimtTileN;
+        g.tile_n = kSimtTileN;
+        return launch_gemm_simt<T>(epi, g, s);
+    };
+    focus_chunk_qk qa{};
+    qa.rows = T_rows; qa.page_size = pl.page_size; qa.n_pages = pl.n_pages; qa.eps = dm.eps;
+    qa.row_pos = pl.row_pos; qa.row_slot = pl.row_slot; qa.q_out = c->q; qa.out_stride = (int64_t)hd; qa.kv_pool = p->kv_pool;
+    T* part = reinterpret_cast<T*>(c->part);
+    qa.q = tc ? c->q : c->part;
+    qa.q_stride = (int64_t)(tc ? hd : dm.qkv);
+    qa.k = tc ? part : part + hd;
+    qa.v = tc ? part + kvd : part + hd + kvd;
+    qa.k_stride = qa.v_stride = (int64_t)(tc ? 2 * kvd : dm.qkv);
+    focus_chunk_attn aa{};
+    aa.n_requests = pl.n_requests; aa.rows = T_rows; aa.max_new = p->max_new; aa.page_size = pl.page_size;
+    aa.n_pages = pl.n_pages; aa.mask_block = p->mask_block; aa.q = c->q; aa.out = c->o;
+    aa.q_stride = aa.out_stride = (int64_t)hd; aa.kv_pool = p->kv_pool; aa.row_offsets = pl.row_offsets;
+    aa.kv_len = pl.kv_len; aa.page_table = pl.page_table;
+    const int nsp = tc ? 0 : 1;  // partial slices the norm kernels still add (CUDA-core path)
+    for (int l = 0; l < dm.L; ++l) {
+        bad = gemm(tc ? EPI_QKV : EPI_PARTIAL, c->h, c->wqkv[l], nullptr, dm.qkv, dm.D, nullptr) < 0 || bad;
+        qa.layer = l;
+        qa.q_norm = p->q_norm ? p->q_norm[l] : nullptr;
+        qa.k_norm = p->k_norm ? p->k_norm[l] : nullptr;
+        if ((rc = focus_chunk_qk_norm_rope(k, &qa, s)) != FOCUS_OK) return rc;
+        if (l == dm.L - 1 && !p->hidden) break;
+        aa.layer = l;
+        if ((rc = focus_chunk_attention(k, &aa, s)) != FOCUS_OK) return rc;
+        bad = gemm(tc ? EPI_RESID : EPI_PARTIAL, c->o, c->wo[l], nullptr, dm.D, (int)hd, c->x_full) < 0 || bad;
+        bad = launch_residual_norm<T>(c->x_full, nullptr, nullptr, T_rows, c->part, nsp, stride, c->x_full, W(c->mlp_norm[l]),
+                                      dm.eps, dm.D, h, s) < 0 || bad;
+        bad = gemm(EPI_SWIGLU, c->h, c->wgate[l], c->wup[l], dm.F, dm.D, nullptr) < 0 || bad;
+        bad = gemm(tc ? EPI_RESID : EPI_PARTIAL, c->act, c->wdown[l], nullptr, dm.D, dm.F, c->x_full) < 0 || bad;
+        const bool last = l + 1 == dm.L;
+        bad = launch_residual_norm<T>(c->x_full, nullptr, nullptr, T_rows, c->part, nsp, stride, last ? p->hidden : c->x_full,
+                                      W(last ? c->final_norm : c->attn_norm[l + 1]), dm.eps, dm.D, last ? nullptr : h, s) < 0 || bad;
+    }
+    return bad || cudaGetLastError() != cudaSuccess ? FOCUS_ERR_CUDA : FOCUS_OK;
+}
+
 void prof_release(focus_ctx* c) {
     for (cudaEvent_t e : c->prof_ev) cudaEventDestroy(e);
     c->prof_ev.clear();
@@ -457,6 +525,7 @@ int focus_init(const focus_model_cfg* cfg, const focus_weights* w, const focus_l
     c->rope_tab = reinterpret_cast<float2*>(base + lay.off[23]);
     c->masked_count = reinterpret_cast<int32_t*>(base + lay.off[24]);
     c->req_order = reinterpret_cast<int32_t*>(base + lay.off[25]);
+    c->zeros = reinterpret_cast<int32_t*>(base + lay.off[26]);
     c->err = reinterpret_cast<int*>(base + lay.off[16]);
     c->att_part_o = reinterpret_cast<float*>(base + lay.off[17]);
     c->att_part_ml = reinterpret_cast<float*>(base + lay.off[18]);
@@ -487,6 +556,7 @@ int focus_init(const focus_model_cfg* cfg, const focus_weights* w, const focus_l
     }
     if (cudaMemcpy(c->inv_freq, inv.data(), inv.size() * sizeof(double), cudaMemcpyHostToDevice) != cudaSuccess ||
         cudaMemset(c->err, 0, sizeof(int)) != cudaSuccess || cudaMemset(c->n_rows, 0, sizeof(int)) != cudaSuccess ||
+        cudaMemset(c->zeros, 0, rows_full * 4) != cudaSuccess ||
         (cfg->dtype == FOCUS_DTYPE_BF16 &&
          cudaMemset(c->att_counters, 0, (size_t)kAttnSplitCap * 4) != cudaSuccess))
         rc = FOCUS_ERR_CUDA;
@@ -546,6 +616,36 @@ int focus_step(focus_ctx* c, const focus_batch* in, const focus_params* p, focus
     nvtxRangePushA("focus_step");
     const int rc = c->cfg.dtype == FOCUS_DTYPE_BF16 ? run_step<bf16>(c, in, p, out, s, k_cap)
                                                     : run_step<float>(c, in, p, out, s, k_cap);
+    nvtxRangePop();
+    return rc;
+}
+
+int focus_prefill(focus_ctx* c, focus_chunk_ctx* k, const focus_prefill_args* p, void* stream) {
+    if (!c || !k || !p || !p->plan) return FOCUS_ERR_INVALID_ARG;
+    const focus_chunk_cfg* g = chunk_cfg(k);
+    if (g->n_layers != c->cfg.n_layers || g->n_q_heads != c->cfg.n_q_heads || g->n_kv_heads != c->cfg.n_kv_heads ||
+        g->head_dim != c->cfg.head_dim || g->dtype != c->cfg.dtype || g->rope_theta != c->cfg.rope_theta)
+        return FOCUS_ERR_INVALID_ARG;
+    const focus_chunk_plan& pl = *p->plan;
+    if (p->max_new < 1 || p->mask_block < 1 || pl.max_rows < 0 || pl.n_requests < 0 ||
+        (pl.max_rows > 0 && pl.n_requests > 0 && !p->tokens) || (pl.n_pages > 0 && !p->kv_pool))
+        return FOCUS_ERR_INVALID_ARG;
+    if ((int64_t)pl.max_rows > (int64_t)c->lim.max_requests * c->lim.max_block) return FOCUS_ERR_LIMITS;
+    // everything the layers check is checked before the first launch, so that a refused call changes nothing
+    const bool bf = c->cfg.dtype == FOCUS_DTYPE_BF16;
+    if (bf && (!c->tc || (pl.page_size != 16 && pl.page_size != 32 && pl.page_size != 64))) return FOCUS_ERR_UNSUPPORTED;
+    auto misaligned = [](const void* x, size_t n) { return (reinterpret_cast<uintptr_t>(x) & (n - 1)) != 0; };
+    if (misaligned(p->tokens, 4) || misaligned(p->kv_pool, 16) || misaligned(p->hidden, 16)) return FOCUS_ERR_INVALID_ARG;
+    for (const void* const* norms : {p->q_norm, p->k_norm})
+        for (int l = 0; norms && l < c->cfg.n_layers; ++l)
+            if (misaligned(norms[l], 16)) return FOCUS_ERR_INVALID_ARG;
+    if (pl.page_size > 0 && (int64_t)pl.n_pages * c->cfg.n_layers * 2 * c->cfg.n_kv_heads >= ((int64_t)1 << 31) / pl.page_size)
+        return FOCUS_ERR_LIMITS;
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev != c->device) return FOCUS_ERR_INVALID_ARG;
+    nvtxRangePushA("focus_prefill");
+    const int rc = bf ? run_prefill<bf16>(c, k, p, static_cast<cudaStream_t>(stream))
+                      : run_prefill<float>(c, k, p, static_cast<cudaStream_t>(stream));
     nvtxRangePop();
     return rc;
 }

@@ -7,7 +7,8 @@ every step and every commit runs through an engine (``FocusEngine``: the library
 ``focus_commit_block``); nothing of the method's arithmetic is here.
 
 Requests arrive with their prompt already in the KV pool (the step serves blocks on top of an exactly
-cached prefix, project page, Overview -- Motivation) and ask for a number of blocks.  Each block of
+cached prefix, project page, Overview -- Motivation), or with its tokens, which are then run through the model
+in chunks at admission (``focus_prefill``), and ask for a number of blocks.  Each block of
 each request goes through the block loop of ``focus_decode_block``: a dense first step, focused steps
 until no position is masked, a dense refresh, and the commit of the block's K/V into the prefix pages.
 Requests sit in the slots of one batch; they are in different phases of that loop at the same time, so
@@ -53,6 +54,7 @@ class Request:
     prompt_len: int               # P: prompt tokens whose K/V are already in the pool
     prompt_pages: List[int]       # pool pages holding them, in position order (owned by the request)
     n_blocks: int                 # blocks to generate (>= 1)
+    prompt_tokens: Optional[List[int]] = None  # the prompt, if it is not in the pool yet (then no prompt_pages)
 
 
 @dataclasses.dataclass
@@ -80,8 +82,10 @@ class IterationStats:
 class FocusEngine:
     """Runs the scheduler's calls on the GPU through a FocusContext (steps and commits on slot views)."""
 
-    def __init__(self, ctx, params, stream: Optional[torch.cuda.Stream] = None):
-        self.ctx = ctx
+    def __init__(self, ctx, params, stream: Optional[torch.cuda.Stream] = None, chunk=None, mask_block: int = 1):
+        """`chunk`: a ChunkContext of the model's geometry, needed for requests that bring prompt tokens;
+        `mask_block`: their attention mask (1 causal, B block-causal in blocks of B positions)."""
+        self.ctx, self.chunk, self.mask_block = ctx, chunk, mask_block
         self.focused = dataclasses.replace(params, forced_keep_frac=-1.0, forced_keep_idx=None,
                                            forced_keep_count=None)
         self.dense = dataclasses.replace(self.focused, forced_keep_frac=1.0)
@@ -109,6 +113,16 @@ class FocusEngine:
 
     def commit(self, view: Dict[str, torch.Tensor]) -> None:
         self.ctx.commit_block(view, stream=self.stream)
+
+    def prefill_rows(self) -> int:
+        """Prompt tokens one call takes (0: no prompts)."""
+        return 0 if self.chunk is None else self.ctx.limits.max_requests * self.ctx.limits.max_block
+
+    def prefill(self, view: Dict[str, torch.Tensor], tokens: torch.Tensor, new_len: torch.Tensor,
+                pages: torch.Tensor) -> None:
+        """Run a chunk of the view's prompts; its new pages are `pages`, in request order."""
+        head = torch.zeros(1, dtype=torch.int32, device=tokens.device)
+        self.ctx.prefill(self.chunk, tokens, new_len, view, pages, head, mask_block=self.mask_block, stream=self.stream)
 
 
 class EffectiveBatchScheduler:
@@ -158,7 +172,13 @@ class EffectiveBatchScheduler:
         S = self.page_size
         if req.n_blocks < 1 or req.prompt_len < 0:
             raise ValueError(f"request {req.rid}: needs n_blocks >= 1 and prompt_len >= 0")
-        if len(req.prompt_pages) != -(-req.prompt_len // S):
+        if req.prompt_tokens is not None:
+            if len(req.prompt_tokens) != req.prompt_len or req.prompt_pages:
+                raise ValueError(f"request {req.rid}: prompt_tokens needs prompt_len tokens and no prompt pages")
+            rows = getattr(self.engine, "prefill_rows", lambda: 0)()
+            if rows < max(1, getattr(self.engine, "mask_block", 1)):
+                raise ValueError(f"request {req.rid}: the engine takes no prompt tokens")
+        elif len(req.prompt_pages) != -(-req.prompt_len // S):
             raise ValueError(f"request {req.rid}: {len(req.prompt_pages)} prompt pages for {req.prompt_len} tokens")
         if -(-(req.prompt_len + req.n_blocks * self.B) // S) > self.max_pages:
             raise ValueError(f"request {req.rid}: prompt plus {req.n_blocks} blocks exceed the page table")
@@ -192,6 +212,7 @@ class EffectiveBatchScheduler:
         rec["block_steps"] = 0
 
     def _admit(self) -> None:
+        fresh: List[int] = []
         while self.waiting and self.waiting[0].arrival <= self.iteration and len(self.slot_req) < self.slots:
             req = self.waiting[0]
             cost = sum(self._cost(r) for r in self.slot_req)
@@ -203,9 +224,43 @@ class EffectiveBatchScheduler:
             rec = {"req": req, "prefix_len": req.prompt_len, "pages": list(req.prompt_pages), "blocks": [],
                    "steps": [], "admitted": self.iteration, "reserved": self.free[:need]}
             del self.free[:need]
+            if req.prompt_tokens is not None:
+                n = -(-req.prompt_len // self.page_size)
+                rec["pages"], rec["reserved"] = rec["reserved"][:n], rec["reserved"][n:]
             self._start_block(rec)
             self.slot_req.append(rec)
             self._write_slot(len(self.slot_req) - 1, rec)
+            if req.prompt_tokens:
+                fresh.append(len(self.slot_req) - 1)
+        if fresh:
+            self._prefill(fresh)
+
+    def _prefill(self, slots: List[int]) -> None:
+        """Run the prompts of these (consecutive) slots through the model, several requests' chunks per call.  A chunk
+        ends at the prompt's end or at a multiple of the mask's block, whose positions see one another."""
+        rows, step = self.engine.prefill_rows(), self.engine.mask_block
+        S, dev = self.page_size, self.tokens.device
+        i32 = dict(dtype=torch.int32)
+        for at in range(0, len(slots), max(1, rows // step)):
+            group = slots[at:at + max(1, rows // step)]
+            a, b = group[0], group[-1] + 1
+            view = self._view(a, b)
+            per = rows // len(group) // step * step
+            prompts = {i: self.slot_req[i]["req"].prompt_tokens for i in group}
+            for i in group:
+                self.prefix_len[i] = 0
+            done = 0
+            while any(len(p) > done for p in prompts.values()):
+                width = min(per, max(len(p) for p in prompts.values()) - done)
+                tokens, new, pages = torch.zeros(b - a, width, **i32), torch.zeros(b - a, **i32), []
+                for i, p in prompts.items():
+                    part = p[done:done + width]
+                    tokens[i - a, : len(part)] = torch.tensor(part, **i32)
+                    new[i - a] = len(part)
+                    if part:
+                        pages += self.slot_req[i]["pages"][-(-done // S):-(-(done + len(part)) // S)]
+                self.engine.prefill(view, tokens.to(dev), new.to(dev), torch.tensor(pages, **i32).to(dev))
+                done += width
 
     # ---- slot moves -----------------------------------------------------------------------------
     def _swap(self, i: int, j: int) -> None:

@@ -310,7 +310,7 @@ int focus_lm_head_conf_noalloc(const float* hidden, int32_t rows, int32_t hidden
  * them: a chunk of new tokens per request (a whole prompt, a slice of one, or a single token) is given
  * pages and rows, its keys and values are written into the pages, and its queries attend over everything
  * the request has cached.  Usual order, per chunk: focus_chunk_plan_rows once, then per layer
- * focus_chunk_qk_norm_rope and focus_chunk_attention.
+ * focus_chunk_qk_norm_rope and focus_chunk_attention; focus_prefill runs a whole model that way.
  *
  * A focus_chunk_ctx holds what the calls need beside their arguments: scratch for attention that is split
  * over the key axis, the rotary frequencies, and a device error word of its own.  Its size does not depend
@@ -452,6 +452,33 @@ typedef struct {
 /* Returns FOCUS_OK, FOCUS_ERR_INVALID_ARG, FOCUS_ERR_LIMITS (N, max_pages_per_req * S > 2^30, or a pool of
  * 2^31 key and value rows or more), FOCUS_ERR_UNSUPPORTED (bf16 page size) or FOCUS_ERR_CUDA. */
 int focus_chunk_attention(focus_chunk_ctx* ctx, const focus_chunk_attn* p, void* stream);
+
+/* A chunk of prompt tokens through the whole model: plan, then per layer the QKV projection, norm + rotation +
+ * cache write and the chunk's attention, O, SwiGLU; the prompt's keys and values end up in the pages a focused
+ * step reads.  focus_chunk_plan_rows, focus_chunk_qk_norm_rope and focus_chunk_attention are called as a user
+ * would call them, with the plan's outputs.
+ *   - `chunk` was made for the same model geometry (layers, heads, head_dim, dtype, rope_theta) on the same device;
+ *   - plan->max_rows <= max_requests * max_block of `ctx` (its workspace holds the rows);
+ *   - plan->prefix_len is updated in place to kv_len (declared const for the plan, which only reads it), so a
+ *     request's chunks follow one another without host work;
+ *   - q_norm / k_norm: HOST arrays of L device pointers [d] T (per-head RMSNorm gains, eps = rms_eps), or NULL.
+ *     The focused step has no such norms: give them only to fill a cache for another decoder;
+ *   - hidden: optional [max_rows, D] float32, the residual stream after the last layer in row order (rows past
+ *     the last are undefined).  Without it the last layer stops at its cache write, all that a prefix needs.
+ * A token id outside [0, V) sets FOCUS_DEVERR_TOKEN_ID in ctx's error word and is read as 0; new_len beyond max_new
+ * sets FOCUS_DEVERR_ROWS there.  Asynchronous, no host sync, can be captured.  Must not overlap another call of
+ * either context.  Returns as focus_step and the chunk calls. */
+typedef struct {
+    const focus_chunk_plan* plan;     /* HOST struct of device pointers */
+    const int32_t* tokens;            /* [N, max_new] token ids, row b's first new_len[b] are used */
+    int32_t max_new;                  /* row length of tokens, bound on new_len (>= 1) */
+    int32_t mask_block;               /* M of focus_chunk_attention */
+    void* kv_pool;                    /* [n_pages, L, 2, Hkv, S, d] T, in place */
+    const void* const* q_norm;
+    const void* const* k_norm;
+    float* hidden;
+} focus_prefill_args;
+int focus_prefill(focus_ctx* ctx, focus_chunk_ctx* chunk, const focus_prefill_args* p, void* stream);
 
 #ifdef __cplusplus
 }
