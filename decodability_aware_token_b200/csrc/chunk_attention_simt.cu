@@ -23,25 +23,31 @@ template <int D, int TR> struct SimtShape {
     static constexpr int KSTR = D + 4;      // padded rows: 16 keys' float4 fall on distinct banks
     static constexpr int PSTR = KEYS + 4;
     static constexpr int Q_F = TR * KSTR, K_F = KEYS * KSTR, V_F = KEYS * D, P_F = TR * PSTR;
-    static constexpr int SMEM = (Q_F + K_F + V_F + P_F + 4 * TR) * 4 + KEYS * 4;
+    static constexpr int SMEM = (Q_F + 2 * (K_F + V_F) + P_F + 4 * TR) * 4 + 2 * KEYS * 8;
 };
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool there) {
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst), n = there ? 16u : 0u;  // 0: the 16 bytes become zero
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
+}
 
 template <typename T, int D, int TR>
 __global__ void __launch_bounds__(kThreads, 2) chunk_attn_simt_kernel(ChunkAttnDev a) {
+    static_assert(sizeof(T) == 4, "copies move float32 rows as they are");
     using S = SimtShape<D, TR>;
     constexpr int KEYS = S::KEYS, KSTR = S::KSTR, PSTR = S::PSTR;
     constexpr bool kTile = TR == 64;
     pdl_entry();
     extern __shared__ __align__(16) float smem[];
-    float* qs = smem;                 // [TR][KSTR]; the output rows at the end of a unit
-    float* ks = qs + S::Q_F;          // [KEYS][KSTR]
-    float* vs = ks + S::K_F;          // [KEYS][D]
-    float* ps = vs + S::V_F;          // [TR][PSTR]
+    float* qs = smem;                 // [TR][KSTR]
+    float* ks = qs + S::Q_F;          // [2][KEYS][KSTR]
+    float* vs = ks + 2 * S::K_F;      // [2][KEYS][D]
+    float* ps = vs + 2 * S::V_F;      // [TR][PSTR]
     float* ms = ps + S::P_F;          // [TR] running maxima
     float* ls = ms + TR;              // [TR] denominators
-    float* al = ls + TR;              // [TR] rescale factors of the block
-    int* vis = reinterpret_cast<int*>(al + TR);  // [TR] visible keys of each row
-    int* ok = vis + TR;               // [KEYS] key present
+    float* al = ls + TR;              // [TR] rescale factors of the block; a piece's weight at the end
+    int* vis = reinterpret_cast<int*>(al + TR);                  // [TR] visible keys of each row
+    long long* row_at = reinterpret_cast<long long*>(vis + TR);  // [2][KEYS] element offset of the key's row, -1: none
     __shared__ ChunkRange rg;
     __shared__ long long red[32];
     __shared__ int last_s;
@@ -49,22 +55,52 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_attn_simt_kernel(ChunkAttnD
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const ChunkShape sh{TR / a.G > 0 ? TR / a.G : 1, kTile ? kFew : 0, kTile ? 0x7fffffff : kFew};
-    chunk_schedule<KEYS, kTile ? 2 : 4>(a, sh, scr_raw, red, &rg);
+    chunk_schedule<KEYS, kTile ? 1 : 4>(a, sh, scr_raw, red, &rg);
     const float sl2 = a.scale * 1.4426950408889634f;
     const T* pool = reinterpret_cast<const T*>(a.kv_pool);
+    const long long v_off = (long long)a.Hkv * a.S * D;
 
     ChunkWalk<KEYS> wk;
     for (wk.start(a, sh, rg); wk.live(); wk.next(a, sh)) {
         const int t0 = wk.k * sh.tok, nrow = min(sh.tok, wk.r.n - t0) * a.G;
+        const int nb = wk.blk1 - wk.blk0;
+        // key `tid` of block blk (threads below KEYS): its page number, then its row's offset
+        auto page_of = [&](int blk) {
+            const int key = blk * KEYS + tid;
+            return tid < KEYS && blk < wk.blk1 && key < wk.r.kv ? a.page_table[(size_t)wk.b * a.max_pages + key / a.S] : -1;
+        };
+        auto place = [&](int blk, int page) {
+            if (tid >= KEYS) return;
+            const int key = blk * KEYS + tid;
+            long long at = -1;
+            if (key < wk.r.kv) {
+                if (page >= 0 && page < a.n_pages)
+                    at = (long long)(((((size_t)page * a.L + a.layer) * 2) * a.Hkv + wk.g) * a.S + key % a.S) * D;
+                else
+                    raise_err(a.err, FOCUS_DEVERR_PAGE_ID);
+            }
+            row_at[(blk & 1) * KEYS + tid] = at;
+        };
+        auto copy = [&](int blk) {
+            float *kd = ks + (blk & 1) * S::K_F, *vd = vs + (blk & 1) * S::V_F;
+#pragma unroll
+            for (int i = tid; i < KEYS * (D / 4); i += kThreads) {
+                const int j = i / (D / 4), c = (i - j * (D / 4)) * 4;
+                const long long at = row_at[(blk & 1) * KEYS + j];
+                const T* src = pool + (at < 0 ? 0 : at) + c;
+                cp_async16(kd + j * KSTR + c, src, at >= 0);
+                cp_async16(vd + j * D + c, at < 0 ? src : src + v_off, at >= 0);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        int page = page_of(wk.blk0);
         __syncthreads();  // the previous unit's shared memory has been read
         for (int i = tid; i < TR * (D / 4); i += kThreads) {
-            const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < nrow) {
-                const int tok = t0 + r / a.G, h = wk.g * a.G + r % a.G;
-                v = load4<T>(reinterpret_cast<const T*>(a.q) + (long long)(wk.r.row0 + tok) * a.q_stride + h * D + c);
-            }
-            *reinterpret_cast<float4*>(qs + r * KSTR + c) = v;
+            const int r = i / (D / 4), c = (i - r * (D / 4)) * 4, tok = r / a.G;
+            const bool in = r < nrow;
+            const T* src = reinterpret_cast<const T*>(a.q) +
+                           (in ? (long long)(wk.r.row0 + t0 + tok) * a.q_stride + (wk.g * a.G + r - tok * a.G) * D + c : 0);
+            cp_async16(qs + r * KSTR + c, src, in);
         }
         if (tid < TR) {
             const int pos = wk.r.kv - wk.r.n + t0 + tid / a.G;
@@ -72,6 +108,10 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_attn_simt_kernel(ChunkAttnD
             ms[tid] = -CUDART_INF_F;
             ls[tid] = 0.f;
         }
+        place(wk.blk0, page);
+        page = page_of(wk.blk0 + 1);
+        __syncthreads();
+        copy(wk.blk0);
         // accumulators: TR = 64: rows 4 ty .. + 3, columns 4 tx + 64 j .. + 3; TR = 8: rows 4 (warp & 1) .. + 3,
         // D / 32 columns from lane * D / 32, over the keys of quarter warp / 2
         constexpr int AC = kTile ? D / 16 : D / 32;
@@ -81,29 +121,17 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_attn_simt_kernel(ChunkAttnD
 #pragma unroll
             for (int j = 0; j < AC; ++j) acc[i][j] = 0.f;
 
-        for (int blk = wk.blk0; blk < wk.blk1; ++blk) {
-            __syncthreads();  // the previous block's K, V, P have been read
-            for (int j = warp; j < KEYS; j += kThreads / 32) {
-                const int key = blk * KEYS + j;
-                int page = -1;
-                if (key < wk.r.kv) {
-                    page = a.page_table[(size_t)wk.b * a.max_pages + key / a.S];
-                    if (page < 0 || page >= a.n_pages) {
-                        if (lane == 0) raise_err(a.err, FOCUS_DEVERR_PAGE_ID);
-                        page = -1;
-                    }
-                }
-                const size_t kr = ((((size_t)max(page, 0) * a.L + a.layer) * 2) * a.Hkv + wk.g) * a.S + key % a.S;
-                const T* kp = pool + kr * D;
-                const T* vp = kp + (size_t)a.Hkv * a.S * D;
-                for (int c = lane * 4; c < D; c += 128) {
-                    const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-                    *reinterpret_cast<float4*>(ks + j * KSTR + c) = page >= 0 ? load4<T>(kp + c) : z;
-                    *reinterpret_cast<float4*>(vs + j * D + c) = page >= 0 ? load4<T>(vp + c) : z;
-                }
-                if (lane == 0) ok[j] = page >= 0;
+        for (int b = 0; b < nb; ++b) {
+            const int blk = wk.blk0 + b;
+            if (b + 1 < nb) {
+                place(blk + 1, page);
+                page = page_of(blk + 2);
             }
-            __syncthreads();
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            __syncthreads();  // this block has landed, the one before has been read
+            if (b + 1 < nb) copy(blk + 1);
+            const float *kb = ks + (blk & 1) * S::K_F, *vb = vs + (blk & 1) * S::V_F;
+            const long long* there = row_at + (blk & 1) * KEYS;
             if constexpr (kTile) {
                 constexpr int KPT = KEYS / 16;
                 const int ty = tid >> 4, tx = tid & 15;
@@ -116,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_attn_simt_kernel(ChunkAttnD
                 for (int c = 0; c < D; c += 4) {
                     float4 kv[KPT];
 #pragma unroll
-                    for (int j = 0; j < KPT; ++j) kv[j] = *reinterpret_cast<const float4*>(ks + (tx + 16 * j) * KSTR + c);
+                    for (int j = 0; j < KPT; ++j) kv[j] = *reinterpret_cast<const float4*>(kb + (tx + 16 * j) * KSTR + c);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float4 q = *reinterpret_cast<const float4*>(qs + (4 * ty + i) * KSTR + c);
@@ -129,6 +157,9 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_attn_simt_kernel(ChunkAttnD
                         }
                     }
                 }
+                bool ok[KPT];
+#pragma unroll
+                for (int j = 0; j < KPT; ++j) ok[j] = there[tx + 16 * j] >= 0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int r = 4 * ty + i;
@@ -136,8 +167,7 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_attn_simt_kernel(ChunkAttnD
                     float mx = -CUDART_INF_F;
 #pragma unroll
                     for (int j = 0; j < KPT; ++j) {
-                        const int key = tx + 16 * j;
-                        s[i][j] = key < lim && ok[key] ? s[i][j] * sl2 : -CUDART_INF_F;
+                        s[i][j] = tx + 16 * j < lim && ok[j] ? s[i][j] * sl2 : -CUDART_INF_F;
                         mx = fmaxf(mx, s[i][j]);
                     }
 #pragma unroll
@@ -172,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_attn_simt_kernel(ChunkAttnD
                     for (int kk = 0; kk < 4; ++kk) {
 #pragma unroll
                         for (int j = 0; j < AC; j += 4) {
-                            const float4 v = *reinterpret_cast<const float4*>(vs + (k4 + kk) * D + 4 * tx + 16 * j);
+                            const float4 v = *reinterpret_cast<const float4*>(vb + (k4 + kk) * D + 4 * tx + 16 * j);
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 const float w = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
@@ -193,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_attn_simt_kernel(ChunkAttnD
                 for (int i = 0; i < RPT; ++i) s[i] = 0.f;
 #pragma unroll 8
                 for (int c = 0; c < D; c += 4) {
-                    const float4 k4 = *reinterpret_cast<const float4*>(ks + key * KSTR + c);
+                    const float4 k4 = *reinterpret_cast<const float4*>(kb + key * KSTR + c);
 #pragma unroll
                     for (int i = 0; i < RPT; ++i) {
                         const float4 q = *reinterpret_cast<const float4*>(qs + (r0 + i) * KSTR + c);
@@ -206,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_attn_simt_kernel(ChunkAttnD
 #pragma unroll
                 for (int i = 0; i < RPT; ++i)
                     ps[(r0 + i) * PSTR + key] =
-                        blk * KEYS + key < vis[r0 + i] && ok[key] ? s[i] * sl2 : -CUDART_INF_F;
+                        blk * KEYS + key < vis[r0 + i] && there[key] >= 0 ? s[i] * sl2 : -CUDART_INF_F;
                 __syncthreads();
                 {
                     const int r = warp;  // eight warps, eight rows
@@ -243,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_attn_simt_kernel(ChunkAttnD
                 for (int k1 = kq; k1 < kq + KEYS / 4; ++k1) {
                     float v[AC];
 #pragma unroll
-                    for (int j = 0; j < AC; ++j) v[j] = vs[k1 * D + lane * AC + j];
+                    for (int j = 0; j < AC; ++j) v[j] = vb[k1 * D + lane * AC + j];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float p = ps[(rb + i) * PSTR + k1];
@@ -253,78 +283,97 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_attn_simt_kernel(ChunkAttnD
                 }
             }
         }
-        // ---- the piece's unnormalised rows to shared memory
-        __syncthreads();
+        __syncthreads();  // maxima and denominators are final; K, V and the queries have been read
+        T* out = reinterpret_cast<T*>(a.out);
+        auto out_ptr = [&](int r) {
+            const int tok = r / a.G;
+            return out + (long long)(wk.r.row0 + t0 + tok) * a.out_stride + (wk.g * a.G + r - tok * a.G) * D;
+        };
+        const bool whole = wk.whole();
+        int c0 = 0, c1 = 0, slot0 = 0;
+        if (!whole) wk.pieces(rg, c0, c1, slot0);
+        auto piece = [&](int c) { return (size_t)(c == c0 ? slot0 : 2 * c); };
+        const size_t mine = piece(blockIdx.x);
+        // four columns of a row: the result, or this piece's unnormalised share
+        auto put = [&](int r, int c, float4 v) {
+            if (whole) {
+                const float inv = ls[r] > 0.f ? 1.f / ls[r] : 0.f;
+                store4<T>(out_ptr(r) + c, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+            } else {
+                __stcg(reinterpret_cast<float4*>(a.part_o + (mine * TR + r) * D + c), v);
+            }
+        };
         if constexpr (kTile) {
             const int ty = tid >> 4, tx = tid & 15;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
+                if (4 * ty + i < nrow)
 #pragma unroll
-                for (int j = 0; j < AC; j += 4)
-                    *reinterpret_cast<float4*>(qs + (4 * ty + i) * KSTR + 4 * tx + 16 * j) =
-                        make_float4(acc[i][j], acc[i][j + 1], acc[i][j + 2], acc[i][j + 3]);
+                    for (int j = 0; j < AC; j += 4)
+                        put(4 * ty + i, 4 * tx + 16 * j, make_float4(acc[i][j], acc[i][j + 1], acc[i][j + 2], acc[i][j + 3]));
         } else {
             float* part = ks;  // [4 key quarters][TR][D]
+            static_assert(4 * TR * D <= 2 * S::K_F || kTile, "the quarters' sums fit in the K buffers");
             const int rb = (warp & 1) * 4;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < AC; ++j) part[((warp >> 1) * TR + rb + i) * D + lane * AC + j] = acc[i][j];
             __syncthreads();
-            for (int i = tid; i < TR * D; i += kThreads)
-                qs[i / D * KSTR + i % D] = (part[i] + part[TR * D + i]) + (part[2 * TR * D + i] + part[3 * TR * D + i]);
-        }
-        __syncthreads();
-        T* out = reinterpret_cast<T*>(a.out);
-        auto out_ptr = [&](int r) {
-            return out + (long long)(wk.r.row0 + t0 + r / a.G) * a.out_stride + (wk.g * a.G + r % a.G) * D;
-        };
-        if (wk.whole()) {
             for (int i = tid; i < nrow * (D / 4); i += kThreads) {
                 const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
-                const float inv = ls[r] > 0.f ? 1.f / ls[r] : 0.f;
-                const float4 v = *reinterpret_cast<const float4*>(qs + r * KSTR + c);
-                store4<T>(out_ptr(r) + c, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float4 x = *reinterpret_cast<const float4*>(part + (q * TR + r) * D + c);
+                    v.x += x.x;
+                    v.y += x.y;
+                    v.z += x.z;
+                    v.w += x.w;
+                }
+                put(r, c, v);
             }
-            continue;
         }
-        // ---- a shared unit: leave the piece in scratch; the last CTA to arrive adds the pieces in order
-        int c0, c1, slot0;
-        wk.pieces(rg, c0, c1, slot0);
-        auto piece = [&](int c) { return (size_t)(c == c0 ? slot0 : 2 * c); };
-        const size_t mine = piece(blockIdx.x);
-        for (int i = tid; i < nrow * (D / 4); i += kThreads) {
-            const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
-            __stcg(reinterpret_cast<float4*>(a.part_o + (mine * TR + r) * D + c),
-                   *reinterpret_cast<const float4*>(qs + r * KSTR + c));
-        }
-        if (tid < nrow) __stcg(reinterpret_cast<float2*>(a.part_ml) + mine * TR + tid, make_float2(ms[tid], ls[tid]));
+        if (whole) continue;
+        // ---- a shared unit: the last CTA to arrive adds the pieces in order
+        float2* pml = reinterpret_cast<float2*>(a.part_ml);
+        if (tid < nrow) __stcg(pml + mine * TR + tid, make_float2(ms[tid], ls[tid]));
         __threadfence();
         __syncthreads();
         if (tid == 0) last_s = atomicInc(reinterpret_cast<unsigned*>(a.counters) + c0, (unsigned)(c1 - c0)) == (unsigned)(c1 - c0);
         __syncthreads();
         if (!last_s) continue;
         __threadfence();
-        for (int i = tid; i < nrow * (D / 4); i += kThreads) {
-            const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
+        const int cnt = c1 - c0 + 1;
+        for (int r = tid; r < nrow; r += kThreads) {  // each row's maximum and denominator over the pieces
             float m = -CUDART_INF_F;
-            for (int p = c0; p <= c1; ++p)
-                m = fmaxf(m, __ldcg(reinterpret_cast<const float2*>(a.part_ml) + piece(p) * TR + r).x);
+#pragma unroll 4
+            for (int p = 0; p < cnt; ++p) m = fmaxf(m, __ldcg(pml + piece(c0 + p) * TR + r).x);
             const float mu = m == -CUDART_INF_F ? 0.f : m;
             float l = 0.f;
+#pragma unroll 4
+            for (int p = 0; p < cnt; ++p) {
+                const float2 x = __ldcg(pml + piece(c0 + p) * TR + r);
+                l = fmaf(x.y, exp2f(x.x - mu), l);
+            }
+            ms[r] = mu;
+            ls[r] = l > 0.f ? 1.f / l : 0.f;
+        }
+        __syncthreads();
+        for (int i = tid; i < nrow * (D / 4); i += kThreads) {
+            const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
+            const float mu = ms[r], inv = ls[r];
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int p = c0; p <= c1; ++p) {
-                const size_t at = piece(p) * TR + r;
-                const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + at);
+#pragma unroll 4
+            for (int p = 0; p < cnt; ++p) {
+                const size_t at = piece(c0 + p) * TR + r;
+                const float f = exp2f(__ldcg(pml + at).x - mu);
                 const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D + c));
-                const float f = exp2f(ml.x - mu);
-                l = fmaf(ml.y, f, l);
                 o.x = fmaf(v.x, f, o.x);
                 o.y = fmaf(v.y, f, o.y);
                 o.z = fmaf(v.z, f, o.z);
                 o.w = fmaf(v.w, f, o.w);
             }
-            const float inv = l > 0.f ? 1.f / l : 0.f;
             store4<T>(out_ptr(r) + c, o.x * inv, o.y * inv, o.z * inv, o.w * inv);
         }
     }

@@ -102,7 +102,7 @@ template <int KEYS, int MINB>
 __device__ void chunk_schedule(const ChunkAttnDev& a, const ChunkShape& sh, long long* scr, long long* red,
                                ChunkRange* out) {
     const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
-    constexpr int kSerial = 4;  // tiles one thread counts by itself
+    constexpr int kSerial = 16;  // tiles one thread counts by itself
     int any_long = 0;
     if (a.N <= nt && a.small_walk) {
         // a request per thread, sums in registers and 32 bits, three barriers; falls through if some request has
