@@ -106,7 +106,7 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
     __syncthreads();
 
     if (warp == kConsumers) {
-        // ---- copies: the whole warp walks, one lane issues
+        // ---- copies: the whole warp walks, lane p issues the block's page p
         const uint32_t el = elect_one();
         const int ppb = kKeys / a.S;  // pages per block
         uint32_t n = 0, d = 0;        // stages filled, units described
@@ -139,15 +139,10 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
             pw.start(a, wk.b, wk.r.kv, wk.blk0 * ppb);
             ok = publish(true);
             for (int blk = wk.blk0; ok && blk < wk.blk1; ++blk, ++n, pw.at += ppb) {
-                pw.need(ppb);
                 const uint32_t st = n % kStages;
-                uint32_t bad = 0;
-                int good = 0;
-                for (int p = 0; p < ppb && pw.in(p); ++p) {
-                    const int page = pw.page(p);
-                    if (page >= 0 && page < a.n_pages) ++good;
-                    else bad |= ((1u << (a.S / 16)) - 1u) << (p * (a.S / 16));
-                }
+                int page;
+                uint32_t bad;
+                const int good = pw.block(a, ppb, page, bad);
                 ok = warp_wait(&empty[st], ((n / kStages) & 1u) ^ 1u, a.err);
                 if (!ok) break;
                 if (el) {
@@ -157,12 +152,9 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
                     mbar_expect_tx(&full[st], (uint32_t)(good * a.S) * 512u);
                 }
                 __syncwarp();
-                for (int p = 0; p < ppb && pw.in(p); ++p) {
-                    const int page = pw.page(p);
-                    if (page >= 0 && page < a.n_pages && el)
-                        tma_load_pool(&pool_map, &full[st], ring + st * kStage + p * a.S * 512, 0, 0,
-                                      (int)(((long long)page * a.L + a.layer) * 2 * a.Hkv) + wk.g);
-                }
+                if (page >= 0)
+                    tma_load_pool(&pool_map, &full[st], ring + st * kStage + lane * a.S * 512, 0, 0,
+                                  (int)(((long long)page * a.L + a.layer) * 2 * a.Hkv) + wk.g);
                 __syncwarp();
             }
         }

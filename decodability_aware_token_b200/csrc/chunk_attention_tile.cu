@@ -292,14 +292,9 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
                 PageWalk pw;
             auto blocks_of = [&](int g, int blk0, int nb) {
                 for (int i = 0; ok && i < nb; ++i, ++n, pw.at += ppb) {
-                    pw.need(ppb);
-                    uint32_t bad = 0;
-                    int good = 0;
-                    for (int p = 0; p < ppb && pw.in(p); ++p) {
-                        const int page = pw.page(p);
-                        if (page >= 0 && page < a.n_pages) ++good;
-                        else bad |= ((1u << (a.S / 16)) - 1u) << (p * (a.S / 16));
-                    }
+                    int page;
+                    uint32_t bad;
+                    const int good = pw.block(a, ppb, page, bad);
                     ok = warp_wait(&empty[st], (turn & 1u) ^ 1u, a.err);
                     if (!ok) break;
                     if (el) {
@@ -310,15 +305,12 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
                         mbar_expect_tx(&full[st], (uint32_t)(good * a.S) * 256u);
                     }
                     __syncwarp();
-                    uint8_t* dst = ring + st * kSlot;
-                    for (int p = 0; p < ppb && pw.in(p); ++p) {
-                        const int page = pw.page(p);
-                        if (page >= 0 && page < a.n_pages && el) {
-                            const int x = (int)(((long long)page * a.L + a.layer) * 2 * a.Hkv) + g;
-                            // (the map's box holds both column halves when a page is a whole block)
-                            tma_load_pool(&pool_map, &full[st], dst + p * a.S * 128, 0, kv, x);
-                            if (a.S < kKeys) tma_load_pool(&pool_map, &full[st], dst + kHalf + p * a.S * 128, 1, kv, x);
-                        }
+                    if (page >= 0) {
+                        uint8_t* dst = ring + st * kSlot + lane * a.S * 128;
+                        const int x = (int)(((long long)page * a.L + a.layer) * 2 * a.Hkv) + g;
+                        // (the map's box holds both column halves when a page is a whole block)
+                        tma_load_pool(&pool_map, &full[st], dst, 0, kv, x);
+                        if (a.S < kKeys) tma_load_pool(&pool_map, &full[st], dst + kHalf, 1, kv, x);
                     }
                     __syncwarp();
                     if (++st == slots) st = 0, ++turn;

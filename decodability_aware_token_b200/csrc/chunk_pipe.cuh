@@ -98,7 +98,7 @@ __device__ __forceinline__ void tma_load_pool(const CUtensorMap* map, uint64_t* 
 }
 
 // The pages of one key block at a time, for a whole warp: the next 32 entries of the request's table row sit in
-// the lanes, so a block's ids cost a shuffle, not a load.
+// the lanes, so a block's ids cost a shuffle, not a load, and each lane issues the copies of its own page.
 struct PageWalk {
     const int32_t* pt;
     int pages, max_pages, at, ahead0, ahead;  // pages that hold keys, row length, next entry, entries ahead0 + lane
@@ -114,12 +114,24 @@ struct PageWalk {
         ahead0 = at;
         ahead = i < max_pages ? pt[i] : -1;
     }
-    // entry `at + p` of the block whose `ppb` entries start at `at` (call need() first)
-    __device__ __forceinline__ void need(int ppb) {
+    // Lane p < ppb gets the id of the block's page p, -1 if there is none (`got` false) or it is not in the pool;
+    // `bad` (every lane): the block's 16-key groups that a bad id covers; returns the number of good pages.
+    __device__ __forceinline__ int block(const ChunkAttnDev& a, int ppb, int& page, uint32_t& bad) {
         if (at + ppb > ahead0 + 32) load();
+        const int lane = threadIdx.x & 31;
+        page = __shfl_sync(0xffffffffu, ahead, (at + lane - ahead0) & 31);
+        const bool in = lane < ppb && at + lane < pages;
+        const bool good = in && page >= 0 && page < a.n_pages;
+        if (!good) page = -1;
+        const uint32_t good_m = __ballot_sync(0xffffffffu, good), bad_m = __ballot_sync(0xffffffffu, in && !good);
+        bad = 0;
+        if (bad_m) {
+            const int groups = a.S / 16;
+            for (int p = 0; p < ppb; ++p)
+                if ((bad_m >> p) & 1u) bad |= ((1u << groups) - 1u) << (p * groups);
+        }
+        return __popc(good_m);
     }
-    __device__ __forceinline__ int page(int p) const { return __shfl_sync(0xffffffffu, ahead, at + p - ahead0); }
-    __device__ __forceinline__ bool in(int p) const { return at + p < pages; }
 };
 
 // One lane of a converged warp.
