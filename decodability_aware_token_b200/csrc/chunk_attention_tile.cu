@@ -46,9 +46,7 @@ constexpr int kSoftWarps = 8;                 // 4 per tile: one thread per quer
 constexpr int kTileThreads = 32 * kSoftWarps + 128;  // then two warps for the copies and one per tile for the MMAs
 constexpr int kCopyWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1, kCopyVWarp = kSoftWarps + 3;  // MMAs of tile t: kMmaWarp + t
 constexpr int kFlags = 16;                    // bad-page flags, one per block in flight
-constexpr float kRaise = 8.f;
-constexpr float kExp1 = 0.69328290f, kExp2 = 0.24221095f, kExp3 = 0.05500893f;
-constexpr int kPolyOf8 = 2;                   // of 8 pairs of weights, those computed on the FMA pipe
+constexpr float kRaise = 1099511627776.f;    // 2^40
 static_assert(kSmem <= 220 * 1024, "shared memory");
 static_assert(kChunkMaxRequests * 8 <= (kKSlots + kVSlots) * kSlot, "the schedule's sums fit in the ring");
 
@@ -160,39 +158,8 @@ __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
     return d;
 }
-__device__ __forceinline__ uint64_t exp2_mufu(uint64_t x) {
+__device__ __forceinline__ uint64_t exp2_2(uint64_t x) {
     return f2(ex2(__uint_as_float((uint32_t)x)), ex2(__uint_as_float((uint32_t)(x >> 32))));
-}
-// 2^x for x <= 8 on the FMA pipe: x = n + f with n the nearest integer (adding 1.5 2^23 leaves it in the low
-// mantissa bits), 2^f by a cubic with value 1 at 0 (least maximal relative error on [-1/2, 1/2], fitted by
-// reweighted least squares: 1.0e-4, a thirty-eighth of the half step the weight is rounded by), n added to
-// the exponent.  x is held at -127, where the result is exactly 0 (1.0's exponent bits cancel): a masked
-// score gets no weight.
-__device__ __forceinline__ float max_nan(float x, float y) {
-    float d;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(x), "f"(y));
-    return d;
-}
-template <int N> __device__ __forceinline__ void exp2_poly_n(uint64_t* x) {
-    uint64_t n[N], f[N], p[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        x[i] = f2(max_nan(__uint_as_float((uint32_t)x[i]), -127.f), max_nan(__uint_as_float((uint32_t)(x[i] >> 32)), -127.f));
-#pragma unroll
-    for (int i = 0; i < N; ++i) n[i] = add2(x[i], f2(12582912.f, 12582912.f));
-#pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = add2(n[i], f2(-12582912.f, -12582912.f));
-#pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = fma2(f[i], f2(-1.f, -1.f), x[i]);
-#pragma unroll
-    for (int i = 0; i < N; ++i) p[i] = fma2(f2(kExp3, kExp3), f[i], f2(kExp2, kExp2));
-#pragma unroll
-    for (int i = 0; i < N; ++i) p[i] = fma2(p[i], f[i], f2(kExp1, kExp1));
-#pragma unroll
-    for (int i = 0; i < N; ++i) p[i] = fma2(p[i], f[i], f2(1.f, 1.f));
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        x[i] = f2((uint32_t)p[i] + ((uint32_t)n[i] << 23), (uint32_t)(p[i] >> 32) + ((uint32_t)(n[i] >> 32) << 23));
 }
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
@@ -512,38 +479,6 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
                     for (int j = 0; j < 64; ++j)
                         if (j >= left || ((bad >> (j >> 4)) & 1u)) s[j] = __float_as_uint(-CUDART_INF_F);
                 }
-                float mx0 = -CUDART_INF_F, mx1 = -CUDART_INF_F, mx2 = -CUDART_INF_F, mx3 = -CUDART_INF_F;
-#pragma unroll
-                for (int j = 0; j < 64; j += 8) {
-                    mx0 = fmaxf(fmaxf(mx0, __uint_as_float(s[j])), __uint_as_float(s[j + 1]));
-                    mx1 = fmaxf(fmaxf(mx1, __uint_as_float(s[j + 2])), __uint_as_float(s[j + 3]));
-                    mx2 = fmaxf(fmaxf(mx2, __uint_as_float(s[j + 4])), __uint_as_float(s[j + 5]));
-                    mx3 = fmaxf(fmaxf(mx3, __uint_as_float(s[j + 6])), __uint_as_float(s[j + 7]));
-                }
-                const float cm = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * sl2;
-                float f = 1.f;
-                if (m == -CUDART_INF_F) {
-                    m = cm;  // no weight has been summed yet: O is zero or not yet written
-                } else if (cm > m + kRaise) {
-                    f = ex2(m - cm);
-                    l *= f;
-                    m = cm;
-                }
-                if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
-                    // O has to hold the previous block's P V
-                    alive = o_wait(sc - 2);
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int c = 0; c < kD; c += 32) {
-                        uint32_t w[32];
-                        tm_ld(o_addr + c, w);
-                        tm_wait(w);
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) * f);
-                        tm_st(o_addr + c, w);
-                    }
-                    tm_wait_st();
-                }
                 // V rows of keys that do not exist may hold anything (a page's tail, an old copy): their weight
                 // is 0, so make them 0 as well
                 if (key0 + kKeys > kv || bad != 0) {
@@ -557,26 +492,62 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
-                const float mu = m == -CUDART_INF_F ? 0.f : m;
-                const uint64_t sl2x2 = f2(sl2, sl2), mux2 = f2(-mu, -mu);
-                uint64_t sum0 = 0, sum1 = 0;
+                const uint64_t sl2x2 = f2(sl2, sl2);
                 uint32_t pk[32];
+                float bsum;
+                auto weights = [&]() {
+                    const float mu = m == -CUDART_INF_F ? 0.f : m;
+                    const uint64_t mux2 = f2(-mu, -mu);
+                    uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    uint64_t x = fma2(f2(s[2 * j], s[2 * j + 1]), sl2x2, mux2);
-                    if ((j & 7) < kPolyOf8) exp2_poly_n<1>(&x);
-                    else x = exp2_mufu(x);
-                    if (j & 1) sum1 = add2(sum1, x);
-                    else sum0 = add2(sum0, x);
-                    pk[j] = pack2(__uint_as_float((uint32_t)x), __uint_as_float((uint32_t)(x >> 32)));
+                    for (int j = 0; j < 32; ++j) {
+                        const uint64_t x = exp2_2(fma2(f2(s[2 * j], s[2 * j + 1]), sl2x2, mux2));
+                        if (j & 1) sum1 = add2(sum1, x);
+                        else sum0 = add2(sum0, x);
+                        pk[j] = pack2(__uint_as_float((uint32_t)x), __uint_as_float((uint32_t)(x >> 32)));
+                    }
+                    const uint64_t sum = add2(sum0, sum1);
+                    bsum = __uint_as_float((uint32_t)sum) + __uint_as_float((uint32_t)(sum >> 32));
+                };
+                if (i > 0) weights();
+                // The reference m only has to keep the weights in range: it is set by the first keys a row sees and
+                // raised when a block's weights sum to more than 2^40 (they are then computed again)
+                if (i == 0 || __any_sync(0xffffffffu, m == -CUDART_INF_F || !(bsum <= kRaise))) {
+                    float cm = -CUDART_INF_F;
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) cm = fmaxf(cm, __uint_as_float(s[j]));
+                    cm *= sl2;
+                    float f = 1.f;
+                    if (m == -CUDART_INF_F) {
+                        m = cm;  // no weight has been summed yet: O is zero or not yet written
+                    } else if (cm > m) {
+                        f = ex2(m - cm);
+                        l *= f;
+                        m = cm;
+                    }
+                    if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+                        // O has to hold the previous block's P V
+                        alive = o_wait(sc - 2);
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < kD; c += 32) {
+                            uint32_t w[32];
+                            tm_ld(o_addr + c, w);
+                            tm_wait(w);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) * f);
+                            tm_st(o_addr + c, w);
+                        }
+                        tm_wait_st();
+                    }
+                    weights();
                 }
+                l += bsum;
                 tm_st(sb, pk);
                 tm_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[t][b]);
-                const uint64_t sum = add2(sum0, sum1);
-                l += __uint_as_float((uint32_t)sum) + __uint_as_float((uint32_t)(sum >> 32));
             }
             alive = alive && o_wait(sc - 1);
             tc_fence_after();
