@@ -41,13 +41,14 @@ constexpr int kKSlots = 4, kVSlots = 5;       // K is used two blocks ahead of V
 constexpr int kUnits = 4;                     // unit descriptors in flight
 constexpr int kQHalf = 128 * 128;             // [128 query vectors][64 columns]
 constexpr int kQTile = 2 * kQHalf;            // one query tile: 32 KB
-constexpr int kSmem = 2 * kQTile + (kKSlots + kVSlots) * kSlot + 1024;
+constexpr int kTurn = 32 * 64;                // bytes a warp turns its output in: 32 rows of 32 columns
+constexpr int kSmem = 2 * kQTile + (kKSlots + kVSlots) * kSlot + 8 * kTurn + 1024;
 constexpr int kSoftWarps = 8;                 // 4 per tile: one thread per query vector
 constexpr int kTileThreads = 32 * kSoftWarps + 128;  // then two warps for the copies and one per tile for the MMAs
 constexpr int kCopyWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1, kCopyVWarp = kSoftWarps + 3;  // MMAs of tile t: kMmaWarp + t
 constexpr int kFlags = 16;                    // bad-page flags, one per block in flight
 constexpr float kRaise = 1099511627776.f;    // 2^40
-static_assert(kSmem <= 220 * 1024, "shared memory");
+static_assert(kSmem <= 226 * 1024 - 512, "shared memory");
 static_assert(kChunkMaxRequests * 8 <= (kKSlots + kVSlots) * kSlot, "the schedule's sums fit in the ring");
 
 __device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* bar, void* dst, int x, int y, int z) {
@@ -182,6 +183,7 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
     uint8_t* q_s = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* k_ring = q_s + 2 * kQTile;
     uint8_t* v_ring = k_ring + kKSlots * kSlot;
+    uint8_t* turn_s = v_ring + kVSlots * kSlot;  // [softmax warp][kTurn]
     __shared__ __align__(8) uint64_t q_full, q_empty, k_full[kKSlots], k_empty[kKSlots], v_full[kVSlots],
         v_empty[kVSlots], s_full[2][2],
         p_full[2][2], o_full[2][2], done_bar[2], u_full[kUnits], u_empty[kUnits];
@@ -551,15 +553,31 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
             }
             alive = alive && o_wait(sc - 1);
             tc_fence_after();
-            bf16* dst = reinterpret_cast<bf16*>(a.out) + (long long)(ud.row0 + tok0 + rt) * a.out_stride +
-                        (ud.g * a.G + r - rt * a.G) * kD;
-            const bool live = r < nrow;
-            auto store = [&](int c, const float (&v)[32], float inv) {  // 32 columns of the row
+            // A lane's row of 32 columns goes through shared memory, so that four lanes write 64 bytes of a row and a
+            // store touches 8 rows, not 32 (16-byte pieces of 32 rows cost the store path four times as long)
+            const int rq = quarter * 32 + (lane >> 2);  // first of the four rows, 8 apart, this lane writes
+            bf16* dst[4];
 #pragma unroll
-                for (int j = 0; j < 32; j += 8)
-                    *reinterpret_cast<uint4*>(dst + c + j) =
-                        make_uint4(pack2(v[j] * inv, v[j + 1] * inv), pack2(v[j + 2] * inv, v[j + 3] * inv),
-                                   pack2(v[j + 4] * inv, v[j + 5] * inv), pack2(v[j + 6] * inv, v[j + 7] * inv));
+            for (int i = 0; i < 4; ++i) {
+                const int rr = rq + 8 * i, tok = rr / a.G;
+                dst[i] = reinterpret_cast<bf16*>(a.out) + (long long)(ud.row0 + tok0 + tok) * a.out_stride +
+                         (ud.g * a.G + rr - tok * a.G) * kD + (lane & 3) * 8;
+            }
+            uint8_t* turn = turn_s + warp * kTurn;
+            auto store = [&](int c, const float (&v)[32], float inv) {  // columns c .. c + 31 of the warp's rows
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    *reinterpret_cast<uint4*>(turn + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
+                        make_uint4(pack2(v[8 * j] * inv, v[8 * j + 1] * inv), pack2(v[8 * j + 2] * inv, v[8 * j + 3] * inv),
+                                   pack2(v[8 * j + 4] * inv, v[8 * j + 5] * inv), pack2(v[8 * j + 6] * inv, v[8 * j + 7] * inv));
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = 8 * i + (lane >> 2);
+                    const uint4 x = *reinterpret_cast<const uint4*>(turn + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4));
+                    if (rq + 8 * i < nrow) *reinterpret_cast<uint4*>(dst[i] + c) = x;
+                }
+                __syncwarp();
             };
             const int c0 = ud.c0, c1 = ud.c1, slot0 = ud.slot0;
             unit_done();
@@ -570,7 +588,7 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
                     for (int c = 0; c < kD; c += 32) {
                         float v[32];
                         tmem_ld32(o_addr + c, v);
-                        if (live) store(c, v, inv);
+                        store(c, v, inv);
                     }
                     tc_fence_before();
                 }
@@ -627,7 +645,7 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
                         v[j + 3] = fmaf(o.w, f, v[j + 3]);
                     }
                 }
-                if (live) store(c, v, inv);
+                store(c, v, inv);
             }
         }
     }
