@@ -1,9 +1,11 @@
 """ctypes mirror of include/focus.h (argument marshalling only)."""
 import ctypes as C
+import importlib.util
 import os
 import struct
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfocus.so")
+MARSHAL_PATH = os.path.join(os.path.dirname(LIB_PATH), "_marshal.so")
 
 FOCUS_OK = 0
 FOCUS_ERR_INVALID_ARG = -1
@@ -118,6 +120,7 @@ ATTN_PACK = struct.Struct("@7if2q6P")
 
 _lib = None
 _enqueue = None
+_marshal = None
 
 
 def load_enqueue():
@@ -133,6 +136,26 @@ def load_enqueue():
             fn.restype = C.c_int
         _enqueue = fns
     return _enqueue
+
+
+def load_marshal():
+    """The extension that reads the chunk operators' tensors in C++ (csrc/marshal.cpp) and the addresses of the three
+    entry points, for it to call.  ImportError if it was not built, or was built for another torch."""
+    global _marshal
+    if _marshal is None:
+        import torch  # (its libraries have to be loaded first)
+        lib = load()
+        if not os.path.exists(MARSHAL_PATH):
+            raise ImportError(f"{MARSHAL_PATH} is missing: build it with `python -m decodability_aware_token_b200.build`")
+        spec = importlib.util.spec_from_file_location(__package__ + "._marshal", MARSHAL_PATH)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        if mod.torch_version != torch.__version__.split("+")[0]:
+            raise ImportError(f"{MARSHAL_PATH} was built for torch {mod.torch_version}: rebuild it")
+        addr = [C.cast(getattr(lib, n), C.c_void_p).value
+                for n in ("focus_chunk_plan_rows", "focus_chunk_qk_norm_rope", "focus_chunk_attention")]
+        _marshal = mod, addr
+    return _marshal
 
 
 def load():

@@ -3,7 +3,8 @@
     python -m decodability_aware_token_b200.build [-v] [--force]
 
 Each .cu under csrc/ compiles to an object under _build/ (in parallel, skipped when up to date),
-then everything links into decodability_aware_token_b200/libfocus.so.
+then everything links into decodability_aware_token_b200/libfocus.so.  csrc/marshal.cpp, the chunk operators'
+host binding, compiles with the host compiler against torch's headers into _marshal.so beside it.
 """
 from __future__ import annotations
 
@@ -13,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +22,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfocus.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -36,6 +39,25 @@ def _nvcc() -> str:
 def _deps() -> list[str]:
     return sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) +
                   glob.glob(os.path.join(ROOT, "include", "*.h")))
+
+
+def build_marshal(force: bool = False) -> str:
+    src = os.path.join(CSRC, "marshal.cpp")
+    newest = max(os.path.getmtime(p) for p in (src, os.path.join(ROOT, "include", "focus.h")))
+    if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= newest:
+        return MARSHAL
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    for p in [*include_paths(), sysconfig.get_paths()["include"], cuda]:
+        cmd += ["-isystem", p]
+    cmd += [src, "-o", MARSHAL, *(f"-L{p}" for p in library_paths()), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on {src}:\n{r.stdout}\n{r.stderr}")
+    return MARSHAL
 
 
 def build(verbose: bool = False, force: bool = False) -> str:
@@ -57,7 +79,9 @@ def build(verbose: bool = False, force: bool = False) -> str:
         return obj, (r.stdout + r.stderr).strip()
 
     with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
+        marshal = ex.submit(build_marshal, force)
         results = list(ex.map(compile_one, sources))
+        marshal.result()
     for obj, log in results:
         if verbose and log:
             print(log)

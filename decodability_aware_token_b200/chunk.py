@@ -41,6 +41,7 @@ class ChunkContext:
     only the outputs they are not given, and can be captured in CUDA graphs.  Two calls of one context must
     not overlap in time; use a context per concurrent stream.
     """
+    _marshal = None
 
     def __init__(self, *, n_layers: int, n_q_heads: int, n_kv_heads: int, head_dim: int, dtype=torch.bfloat16,
                  max_requests: int, max_pages_per_req: int, rope_theta: float = 10000.0, device="cuda"):
@@ -52,6 +53,7 @@ class ChunkContext:
             raise ValueError(f"device {dev}: a CUDA device is needed")
         self._lib = _abi.load()
         self._enqueue = _abi.load_enqueue()
+        self._marshal, self._entry = _abi.load_marshal()
         self.device = torch.device("cuda", torch.cuda.current_device() if dev.index is None else dev.index)
         self.dtype = dtype
         self._index = self.device.index
@@ -73,7 +75,18 @@ class ChunkContext:
                          torch.zeros(max_rows, **kw), torch.zeros(max_rows, **kw), torch.zeros(1, **kw))
 
     # ---- checks -----------------------------------------------------------------------------------------
-    # The fast tests below decide; _need and _heads_error only word the refusal.
+    # A call whose outputs are given and whose device is current goes through csrc/marshal.cpp, which makes the
+    # checks below in C++ and returns None where one fails.  The Python path then makes them again: the fast tests
+    # decide, _need and _heads_error word the refusal.
+    def _stream(self, stream, where):
+        if not self._ctx.value:
+            raise ValueError(f"{where}: the context is closed")
+        if stream is None:
+            return _raw_stream(self._index)
+        if stream.device_index != self._index:
+            raise ValueError(f"{where}: the stream is on cuda:{stream.device_index}, the context on {self.device}")
+        return stream.cuda_stream
+
     def _ints(self, t, name, shape):
         if not (isinstance(t, torch.Tensor) and t.dtype is _I32 and t.get_device() == self._index and
                 t.shape == shape and t.is_contiguous()):
@@ -122,12 +135,7 @@ class ChunkContext:
         return s[0], s[4], p
 
     def _call(self, which, args, where, stream):
-        if not self._ctx.value:
-            raise ValueError(f"{where}: the context is closed")
-        fn = self._enqueue[which]
-        if stream is not None and stream.device_index != self._index:
-            raise ValueError(f"{where}: the stream is on cuda:{stream.device_index}, the context on {self.device}")
-        s = _raw_stream(self._index) if stream is None else stream.cuda_stream
+        fn, s = self._enqueue[which], self._stream(stream, where)
         if _current_device() == self._index:
             rc = fn(self._ctx, args, s)
         else:
@@ -145,8 +153,18 @@ class ChunkContext:
         prefix_len, new_len [N] int32; page_table [N, max_pages_per_req] int32, new pages are written into it;
         free_pages [F] int32, taken from index free_head [1] int32 on.  `max_rows` (or the size of `out`)
         bounds the rows.  A request that does not fit gets no rows: row_offsets tells."""
+        where = "focus_chunk_plan_rows"
+        if self._marshal and out is not None and max_rows is None and _current_device() == self._index:
+            rc = self._marshal.plan(
+                self._entry[0], self._ctx.value, self._stream(stream, where), self._index, self.limits.max_pages_per_req,
+                page_size, n_pages, prefix_len, new_len, page_table, free_pages, free_head, out.row_offsets, out.kv_len,
+                out.row_req, out.row_pos, out.row_slot, out.free_next)
+            if rc == 0:
+                return out
+            if rc is not None:
+                _check(rc, where)
         args, out = self._plan_args(prefix_len, new_len, page_table, free_pages, free_head, page_size, n_pages, max_rows, out)
-        self._call(0, args, "focus_chunk_plan_rows", stream)
+        self._call(0, args, where, stream)
         return out
 
     def _plan_args(self, prefix_len, new_len, page_table, free_pages, free_head, page_size, n_pages, max_rows, out):
@@ -172,6 +190,16 @@ class ChunkContext:
         """Norm (with the gains given), rotate, store K and V at row_slot; returns the queries
         (focus_chunk_qk_norm_rope).  q [rows, Hq, d], k and v [rows, Hkv, d] may be views of one fused
         projection; rows with row_pos < 0 are skipped."""
+        where = "focus_chunk_qk_norm_rope"
+        if self._marshal and out is not None and _current_device() == self._index:
+            rc = self._marshal.qk(
+                self._entry[1], self._ctx.value, self._stream(stream, where), self._index, self._elt == 2, self.n_q_heads,
+                self.n_kv_heads, self.head_dim, self.cfg.n_layers, layer, eps, q, k, v, kv_pool, row_pos, row_slot, q_norm,
+                k_norm, out)
+            if rc == 0:
+                return out
+            if rc is not None:
+                _check(rc, where)
         rows, hq, hkv = q.shape[0], self.n_q_heads, self.n_kv_heads
         qp, qs = self._heads(q, "q", rows, hq)
         kp, ks = self._heads(k, "k", rows, hkv)
@@ -184,7 +212,7 @@ class ChunkContext:
         gk = self._gain(k_norm, "k_norm") if k_norm is not None else 0
         args = _abi.QK_PACK.pack(rows, layer, page_size, n_pages, eps, qs, ks, vs, os_, qp, kp, vp, gq, gk,
                                  self._ints(row_pos, "row_pos", (rows,)), self._ints(row_slot, "row_slot", (rows,)), op, pool)
-        self._call(1, args, "focus_chunk_qk_norm_rope", stream)
+        self._call(1, args, where, stream)
         return out
 
     def _gain(self, t, name):
@@ -202,6 +230,17 @@ class ChunkContext:
         """Attention of the chunk's queries [rows, Hq, d] over the cached keys and values
         (focus_chunk_attention).  `max_new` bounds the rows of a request (default: all rows); a tight bound
         saves work.  mask_block 1 is the causal mask, B the block-causal mask of blocks of B positions."""
+        where = "focus_chunk_attention"
+        if (self._marshal and out is not None and max_new is not None and _current_device() == self._index and
+                (scale is None or scale > 0)):
+            rc = self._marshal.attention(
+                self._entry[2], self._ctx.value, self._stream(stream, where), self._index, self._elt == 2, self.n_q_heads,
+                self.n_kv_heads, self.head_dim, self.cfg.n_layers, self.limits.max_pages_per_req, layer, max_new, mask_block,
+                0.0 if scale is None else scale, q, kv_pool, row_offsets, kv_len, page_table, out)
+            if rc == 0:
+                return out
+            if rc is not None:
+                _check(rc, where)
         rows, n, hq = q.shape[0], kv_len.shape[0], self.n_q_heads
         qp, qs = self._heads(q, "q", rows, hq)
         if out is None:
@@ -217,7 +256,7 @@ class ChunkContext:
         args = _abi.ATTN_PACK.pack(n, rows, max_new, page_size, n_pages, layer, mask_block, scale, qs, os_, qp, pool,
                                    self._ints(row_offsets, "row_offsets", (n + 1,)), self._ints(kv_len, "kv_len", (n,)),
                                    self._ints(page_table, "page_table", (n, self.limits.max_pages_per_req)), op)
-        self._call(2, args, "focus_chunk_attention", stream)
+        self._call(2, args, where, stream)
         return out
 
     # ---- state ------------------------------------------------------------------------------------------
