@@ -39,6 +39,10 @@ struct ChunkAttnDev {
     long long q_stride, out_stride;  // elements
     int N, rows, max_new, Hq, Hkv, G, L, layer, S, n_pages, max_pages, mask_block;
     float scale;
+    bool more;        // bf16: the tile kernel follows the few-row kernel and may be launched at once.  Otherwise nothing is
+                      // launched before the work is handed out: the next operator's CTAs, waiting on the SMs, cost more
+                      // than their early launch gives (norm and rotation, then attention, repeated: 32 single tokens
+                      // 26.0 -> 23.8 us, 8192-token prompt 373 -> 360)
     bool small_walk;  // the launch's key blocks, and their products with the CTA count, fit 31 bits
     // scratch of units whose key walk is split over CTAs: slot 2c / 2c + 1 is CTA c's first / last piece
     float* part_o;
@@ -46,7 +50,9 @@ struct ChunkAttnDev {
     int* counters;   // [kChunkCtas] arrivals at the unit whose first piece is CTA c's; zero between launches
     int* err;
 };
-// bf16 models: requests of at most kChunkFewRows query vectors per KV head (single tokens) and the others
+// bf16 models: requests of at most kChunkFewRows query vectors per KV head (single tokens) go to one kernel, the others
+// to the tile kernel.  16 is what one mma.sync tile holds.  Measured, few / tile kernel, 32/8 heads: 256 single tokens
+// 204 / 290 us, 256 requests of 4 tokens (16 vectors) 237 / 296 us, 32 of them 47 / 56 us.
 constexpr int kChunkFewRows = 16;
 constexpr int kChunkTileRows = 256;  // query vectors per unit of the tile kernel
 int launch_chunk_attention_few(const ChunkAttnDev& a, int sms, cudaStream_t s);

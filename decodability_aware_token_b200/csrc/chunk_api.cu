@@ -147,8 +147,11 @@ int focus_chunk_get_device_error(focus_chunk_ctx* c, int32_t* bits) {
     int prev = -1, v = 0;
     cudaGetDevice(&prev);
     bool ok = cudaSetDevice(c->device) == cudaSuccess && cudaDeviceSynchronize() == cudaSuccess &&
-              cudaMemcpy(&v, c->err, 4, cudaMemcpyDeviceToHost) == cudaSuccess && cudaMemset(c->err, 0, 4) == cudaSuccess &&
-              cudaDeviceSynchronize() == cudaSuccess;
+              cudaMemcpy(&v, c->err, 4, cudaMemcpyDeviceToHost) == cudaSuccess;
+    // a launch that gave up may have left arrivals behind: the counters are zero again as well
+    const Layout l = plan_layout(&c->cfg);
+    const size_t words = (v & FOCUS_DEVERR_TIMEOUT) ? l.part_ml - l.words : sizeof(int);
+    ok = ok && cudaMemset(c->err, 0, words) == cudaSuccess && cudaDeviceSynchronize() == cudaSuccess;
     if (prev >= 0) cudaSetDevice(prev);
     if (!ok) return FOCUS_ERR_CUDA;
     if (bits) *bits = v;
@@ -257,8 +260,11 @@ int focus_chunk_attention(focus_chunk_ctx* c, const focus_chunk_attn* p, void* s
     int n;
     if (bf) {
         // each kernel serves the requests on its side of kChunkFewRows query vectors and skips the others
-        n = a.G <= kChunkFewRows ? launch_chunk_attention_few(a, c->sms, s) : 0;
-        if (n >= 0 && (int64_t)a.max_new * a.G > kChunkFewRows) n = launch_chunk_attention_tile(a, c->sms, s);
+        const bool tile = (int64_t)a.max_new * a.G > kChunkFewRows;
+        ChunkAttnDev few = a;
+        few.more = tile;
+        n = a.G <= kChunkFewRows ? launch_chunk_attention_few(few, c->sms, s) : 0;
+        if (n >= 0 && tile) n = launch_chunk_attention_tile(a, c->sms, s);
     } else {
         n = c->cfg.head_dim == 64 ? launch_chunk_attention_simt<float, 64>(a, c->sms, s)
                                   : launch_chunk_attention_simt<float, 128>(a, c->sms, s);

@@ -5,14 +5,16 @@
 // Bound by memory: each cached key and value is read once, so the design is a copy that never stops.  One CTA
 // per SM walks its equal share of the batch's key blocks (chunk_work.cuh); one warp issues the pages of 64-key
 // blocks by TMA into a ring of six 32 KB stages and runs on across unit ends.  Two groups of four warps consume
-// alternate units, 16 keys of a block per warp: a group keeps up with the copies (600 to 700 ns a block of
-// compute against 740 at the copy rate), and while it joins its warps' results and writes them, the other one
-// is already at the next unit.  A warp keeps its own running maximum, denominator and 16 x 128 output, so
-// nothing is exchanged while a unit lasts.  Pieces of a unit that spans CTAs are joined by the CTA that finishes
-// last, in block order.
+// alternate units, 16 keys of a block per warp: a group keeps up with the copies, and while it joins its warps'
+// results and writes them, the other one is already at the next unit.  A warp keeps its own running maximum, denominator
+// and 16 x 128 output, so nothing is exchanged while a unit lasts.  Pieces of a unit that spans CTAs are joined by the
+// CTA that finishes last, in block order.  Measured: 256 requests of 512 to 2048 tokens, 32/8 heads, 208 us = 6.1 TB/s,
+// 94 % of the copy rate; 32 requests of 256 to 1024 tokens, 16/8 heads, 20.7 us against 11.7 at that rate (start-up, unit
+// ends and the joins of split units).
 //
-// Weights are rounded to bf16 for the product with V (relative 2^-9 each, as the values' own type); maxima,
-// denominators and outputs are float32.  The running maximum is raised only by more than 2^8.
+// Weights are rounded to bf16 for the product with V, the values' own type (off by at most 2^-8 of a weight); maxima,
+// denominators and outputs are float32.  The running maximum is raised only by more than 8 (weights up to 2^8),
+// which spares most blocks the rescaling of O.
 #include <math_constants.h>
 
 #include "chunk_pipe.cuh"
@@ -38,7 +40,7 @@ constexpr int kQBytes = kRows * kQRow;
 constexpr int kFewSmem = kStages * kStage + kConsumers * kJoinF * 4 + kUnits * kQBytes + 1024;
 static_assert(kFewSmem <= 224 * 1024, "shared memory");
 static_assert(kChunkMaxRequests * 8 <= kStages * kStage, "the schedule's sums fit in the ring");
-constexpr float kRaise = 8.f;
+constexpr float kRaise = 8.f;                // in units of log2
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -70,7 +72,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 __global__ void __launch_bounds__(kFewThreads, 1)
 chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev a) {
-    pdl_trigger();
+    if (a.more) pdl_trigger();
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float* join = reinterpret_cast<float*>(ring + kStages * kStage);  // [warp][2 rows][128]
@@ -158,6 +160,7 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
                 __syncwarp();
             }
         }
+        pdl_trigger();
         if (ok && publish(false)) publish(false);  // an end for each group
         // never leave with copies in flight
         for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i) warp_wait(&full[i % kStages], (i / kStages) & 1u, a.err);

@@ -5,18 +5,29 @@
 // Unit: request b, KV head g and up to 256 query vectors (token r / G, head r % G) in two tiles of up to
 // 128.  Keys come in blocks of 64 through rings of four K and five V slots of 16 KB, each filled from
 // whole pages by TMA (two 64-column halves, 128-byte swizzle).  Per tile t and block i:
-//   S_t = Q_t K_i^T     tcgen05.mma 128 x 128 x 128, both operands in shared memory, into TMEM
-//   softmax             one warpgroup per tile, one thread per query vector: the 128 scores from TMEM,
-//                       running maximum and denominator in registers, P = 2^(s - m) as bf16 back into TMEM
-//                       over S_t (64 of its 128 columns)
-//   O_t += P_t V_i      tcgen05.mma 128 x 128 x 128, P from TMEM, V MN-major straight from the page tile
-// The MMA thread issues PV_0(i), S_0(i+1), PV_1(i), S_1(i+1): while one tile is in its softmax the tensor core
-// works for the other.  TMEM: S_0, S_1, O_0, O_1, 128 fp32 columns each, all 512.
+//   S_t = Q_t K_i^T     tcgen05.mma 128 x 64 x 128, both operands in shared memory, into one of the tile's two
+//                       S buffers in TMEM
+//   softmax             one warpgroup per tile, one thread per query vector: the 64 scores from TMEM, reference m
+//                       and denominator in registers, P = 2^(s - m) as bf16 back into TMEM over S_t
+//   O_t += P_t V_i      tcgen05.mma 128 x 128 x 64, P from TMEM, V MN-major straight from the page tile
+// One warp per tile issues its MMAs, S_t(i + 2) behind P V_t(i): the next block's scores are there when the
+// softmax has finished with this one, and while one tile is in its softmax the tensor core works for the other.
+// TMEM: two S buffers of 64 columns per tile, O_0, O_1 of 128, all 512 columns.
 //
-// The running maximum is raised only when a block exceeds it by more than 2^8; O and the denominator are then
-// rescaled in TMEM (S_t(i) was issued behind PV_t(i-1), so O is complete when the scores are).  Weights are
-// at most 2^8, sums are float32, and the softmax is the same.  P is rounded to bf16 (relative 2^-9 per
-// weight, as the storage type of the values it multiplies); the denominator sums the unrounded weights.
+// softmax(s) does not change with the reference that is subtracted, so m only has to keep 2^(s - m) in range: it
+// is the first visible block's maximum, and it is raised to the running one (O and the denominator rescaled in TMEM and
+// registers, the block's weights computed again) when a block's weights sum to more than 2^40.  That takes the
+// 64-step maximum out of most blocks.  2^24 blocks of at most 2^40 sum to 2^64, which leaves O in range for |V| < 2^64.
+// P is rounded to bf16, the type of the values it multiplies (off by at most 2^-8 of a weight); the denominator
+// sums the unrounded weights in float32.
+//
+// Bound by the exponentials and the tensor core together, under the power limit: per block and tile, 128 x 64
+// exponentials at 8.3 cycles a warp instruction and quarter of an SM take 530 cycles, the two products 52 cycles per
+// 16 columns of S and 66 per 16 keys of O, 680 for both, so two tiles keep the tensor core busy 1360 cycles of a
+// block's time with the softmax beside it.  Measured: prompt of 8192 tokens, 16/8 heads, 303 us (907 TFLOP/s at 1.3 to
+// 1.55 GHz, where the card's power limit holds it); two chunks of 1024 tokens over 65000 cached, 32/8 heads, 2450 us.
+// Why this shape: with 128 keys a block only one S buffer per tile fits in TMEM, and the prompt took 368 us; with
+// one MMA warp for both tiles and one S buffer 347 us; with two threads per query vector the scores spill.
 //
 // Every mbarrier wait is bounded; on expiry the role flags FOCUS_DEVERR_TIMEOUT and stops issuing, copies and
 // MMAs in flight are waited for (bounded), and TMEM is released.
@@ -47,7 +58,7 @@ constexpr int kSoftWarps = 8;                 // 4 per tile: one thread per quer
 constexpr int kTileThreads = 32 * kSoftWarps + 128;  // then two warps for the copies and one per tile for the MMAs
 constexpr int kCopyWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1, kCopyVWarp = kSoftWarps + 3;  // MMAs of tile t: kMmaWarp + t
 constexpr int kFlags = 16;                    // bad-page flags, one per block in flight
-constexpr float kRaise = 1099511627776.f;    // 2^40
+constexpr float kRaise = 1099511627776.f;     // 2^40
 static_assert(kSmem <= 226 * 1024 - 512, "shared memory");
 static_assert(kChunkMaxRequests * 8 <= (kKSlots + kVSlots) * kSlot, "the schedule's sums fit in the ring");
 
@@ -170,7 +181,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 // The four warps of tile t meet at named barrier 1 + t.
 __device__ __forceinline__ void sync_tile(int t) { named_sync<128>(1 + t); }
 
-// Registers by role: 384 threads start with 168 each (64512); the softmax warps hold a row's 128 scores, the
+// Registers by role: 384 threads start with 168 each (64512); the softmax warps hold a row's 64 scores and weights, the
 // last warpgroup (copies, MMAs) needs few: 256 x 208 + 128 x 88 = 64512.
 constexpr int kSoftRegs = 208, kIssueRegs = 88;
 static_assert(32 * kSoftWarps * kSoftRegs + 128 * kIssueRegs <= kTileThreads * 168, "register split");
@@ -178,7 +189,6 @@ static_assert(32 * kSoftWarps * kSoftRegs + 128 * kIssueRegs <= kTileThreads * 1
 __global__ void __launch_bounds__(kTileThreads, 1)
 chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_constant__ CUtensorMap q_map,
                        ChunkAttnDev a) {
-    pdl_trigger();
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* q_s = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* k_ring = q_s + 2 * kQTile;
@@ -237,9 +247,14 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
     pdl_wait();
 
     const int tpt = 128 / a.G;  // tokens per tile
+    // The copies leave the query rows past G tokens' heads alone; whatever is there would send its warp through the
+    // recomputation below in every block, so make them zero.
+    const int dead = 128 - a.G * tpt;
+    for (int i = threadIdx.x; i < 4 * dead * 8; i += kTileThreads)
+        *reinterpret_cast<uint4*>(q_s + i / (dead * 8) * kQHalf + a.G * tpt * 128 + i % (dead * 8) * 16) = make_uint4(0, 0, 0, 0);
     const ChunkShape sh{2 * tpt, a.G <= kChunkFewRows ? kChunkFewRows : 0, 0x7fffffff};
     chunk_schedule<kKeys, 4>(a, sh, reinterpret_cast<long long*>(k_ring), red, &rg);
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the rings held the schedule's sums
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the rings held the schedule's sums (and the zeros)
     __syncthreads();
 
     // the copy thread walks the range; the others read what it has found
@@ -258,7 +273,7 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
             int st = 0;             // n % slots
             uint32_t turn = 0;      // n / slots
             bool ok = true;
-                PageWalk pw;
+            PageWalk pw;
             auto blocks_of = [&](int g, int blk0, int nb) {
                 for (int i = 0; ok && i < nb; ++i, ++n, pw.at += ppb) {
                     int page;
@@ -513,7 +528,7 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
                 };
                 if (i > 0) weights();
                 // The reference m only has to keep the weights in range: it is set by the first keys a row sees and
-                // raised when a block's weights sum to more than 2^40 (they are then computed again)
+                // raised when a block's weights sum to more than 2^40 (they are then computed again).
                 if (i == 0 || __any_sync(0xffffffffu, m == -CUDART_INF_F || !(bsum <= kRaise))) {
                     float cm = -CUDART_INF_F;
 #pragma unroll

@@ -4,11 +4,11 @@
 // (at least one, so that rows that see nothing are still written).  The units of a launch, in the order
 // b, g, k, form one line of W blocks, and CTA c of C takes an equal share of it (W / C blocks, the first W % C
 // CTAs one more): every CTA walks the same number of key blocks whatever the lengths are, and at most its
-// first and its last unit are shared with neighbours.  Shared units write unnormalised partial results; the CTA that arrives last adds
-// them in block order, so the result does not depend on the order of arrival.
+// first and its last unit are shared with neighbours.  Shared units write unnormalised partial results; the CTA that
+// arrives last adds them in block order, so the result does not depend on the order of arrival.
 //
-// Each CTA finds its own range from the lengths alone (a scan over the requests in shared memory, about a
-// microsecond): no scheduling kernel, no host copy of the lengths.
+// Each CTA finds its own range from the lengths alone, by a scan over the requests (in registers when every thread
+// has at most one): no scheduling kernel, no host copy of the lengths.
 #pragma once
 #include "chunk.h"
 

@@ -425,7 +425,8 @@ int focus_chunk_qk_norm_rope(focus_chunk_ctx* ctx, const focus_chunk_qk* p, void
  * with float32 scores, maxima, sums and accumulators; bf16 weights are rounded once before the product
  * with V.  A row that sees no key (kv_len[b] < n_b) gets zeros; rows of no request stay as they were.
  * Cache entries no row of a request sees, and pages' tails past kv_len, may hold anything, NaN included;
- * V of a key that some row of the request sees has to be finite.
+ * V of a key that some row of the request sees has to be finite, in bf16 below 2^64 (sums of weights times V are
+ * kept unnormalised, with weights up to 2^40).
  * A row range outside [0, rows], decreasing, or longer than max_new sets FOCUS_DEVERR_ROWS and skips the
  * request; kv_len outside [0, max_pages_per_req * S] sets FOCUS_DEVERR_PREFIX and skips it; a page id
  * outside [0, n_pages) sets FOCUS_DEVERR_PAGE_ID and its keys are not attended to.  Row ranges of different
