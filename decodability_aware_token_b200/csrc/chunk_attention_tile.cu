@@ -625,7 +625,8 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
                 }
                 tc_fence_before();
             }
-            __stcg(pm + mine * 128 + r, make_float2(m, l));
+            // (a row whose scores are all NaN has no maximum; a NaN there keeps its piece from being skipped as empty)
+            __stcg(pm + mine * 128 + r, make_float2(l == l ? m : l, l));
             __threadfence();
             sync_tile(t);
             if (r == 0)

@@ -10,8 +10,8 @@ Tolerances.  u is half a step of the stored type relative to the value: 2^-8 for
   off by at most (d + 6) 2^-24 B, which moves each weight by twice that relative (itself and the denominator);
   sums over n keys add (n / 16 + 64) 2^-24 (chains of at most n / 16 terms before they are joined, and the
   joins); float32 weights are good to 2^-22.  bf16 weights are rounded before the product with V (2^-8 each, the
-  denominator is not) and a quarter of them comes from a cubic (1.1e-4, both sides of the quotient: 2.2e-4).
-  |error| <= u |out| + A (2 (d + 6) 2^-24 B + (n / 16 + 64) 2^-24 + 2^-22 + [bf16] (2^-8 + 2.2e-4)).
+  denominator is not).
+  |error| <= u |out| + A (2 (d + 6) 2^-24 B + (n / 16 + 64) 2^-24 + 2^-22 + [bf16] 2^-8).
 """
 import math
 import random
@@ -315,7 +315,7 @@ class Batch:
             w = w / w.sum(-1, keepdim=True).clamp(min=1e-300)
             want, A = w @ v[:, None], w @ v[:, None].abs()
             tol = U[self.dt] * want.abs() + A * (2 * (self.d + 6) * E * big + (kv / 16 + 64) * E + 2.0 ** -22 +
-                                                 (2.0 ** -8 + 2.2e-4 if self.dt == BF else 0))
+                                                 (2.0 ** -8 if self.dt == BF else 0))
             err = (got.reshape(n, self.hkv, G, self.d).permute(1, 2, 0, 3) - want).abs()
             assert bool((err <= tol).all()), (b, n, kv, float((err - tol).max()))
 
