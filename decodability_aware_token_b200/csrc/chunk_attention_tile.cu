@@ -530,8 +530,8 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
                 // The reference m only has to keep the weights in range: it is set by the first keys a row sees and
                 // raised when a block's weights sum to more than 2^40 (they are then computed again), by the rows
                 // that need it alone: what a row gets does not depend on its neighbours.
-                const bool need = i == 0 || m == -CUDART_INF_F || !(bsum <= kRaise);
-                if (__any_sync(0xffffffffu, need)) {
+                if (i == 0 || __any_sync(0xffffffffu, m == -CUDART_INF_F || !(bsum <= kRaise))) {
+                    const bool need = i == 0 || m == -CUDART_INF_F || !(bsum <= kRaise);
                     float cm = -CUDART_INF_F;
 #pragma unroll
                     for (int j = 0; j < 64; ++j) cm = fmaxf(cm, __uint_as_float(s[j]));
