@@ -429,7 +429,9 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
                     commit_one(el, &v_empty[vs]);
                     next_v();
                     if (j + 2 < nb) {
-                        ok = k_here();
+                        // (only when P V is done: MMAs issued into a full queue hold up the softmax warp of this SM
+                        // quarter; 8192-token prompt 297 -> 290 us)
+                        ok = k_here() && warp_wait(&o_full[t][b], ((pc - 1) >> 1) & 1u, a.err);
                         if (!ok) break;
                         tc_fence_after();
                         scores();
