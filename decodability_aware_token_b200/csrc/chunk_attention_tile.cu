@@ -21,13 +21,15 @@
 // P is rounded to bf16, the type of the values it multiplies (off by at most 2^-8 of a weight); the denominator
 // sums the unrounded weights in float32.
 //
-// Bound by the exponentials and the tensor core together, under the power limit: per block and tile, 128 x 64
-// exponentials at 8.3 cycles a warp instruction and quarter of an SM take 530 cycles, the two products 52 cycles per
-// 16 columns of S and 66 per 16 keys of O, 680 for both, so two tiles keep the tensor core busy 1360 cycles of a
-// block's time with the softmax beside it.  Measured: prompt of 8192 tokens, 16/8 heads, 303 us (907 TFLOP/s at 1.3 to
-// 1.55 GHz, where the card's power limit holds it); two chunks of 1024 tokens over 65000 cached, 32/8 heads, 2450 us.
+// Bound by the tensor core and the softmax side by side: a pair of blocks keeps the tensor core for 1360 cycles (S at
+// 52 a K step of 16, its operands read from shared memory as fast as that goes, P V at 66) and the exponential unit
+// for 1062 of the 1800 that it takes.  The 8192-token prompt (16/8 heads) takes 279 us, 985 TFLOP/s at 1.5 to 1.6 GHz,
+// where the card's power management holds it.  When it took 290, leaving out the MMAs left 265, leaving out the
+// softmax's arithmetic 283, and leaving out both, which is the copies out of L2, 205.  Two chunks of 1024 tokens over
+// 65000 cached, 32/8 heads: 2230 us in short runs, 2450 in long ones.
 // Why this shape: with 128 keys a block only one S buffer per tile fits in TMEM, and the prompt took 368 us; with
-// one MMA warp for both tiles and one S buffer 347 us; with two threads per query vector the scores spill.
+// one MMA warp for both tiles and one S buffer 347 us; with two threads per query vector (16 softmax warps) 325 against
+// 290; with the two tiles' exponentials kept half a block apart 302.
 //
 // Every mbarrier wait is bounded; on expiry the role flags FOCUS_DEVERR_TIMEOUT and stops issuing, copies and
 // MMAs in flight are waited for (bounded), and TMEM is released.
@@ -641,30 +643,36 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
             sync_tile(t);
             if (!last_s[t]) continue;
             __threadfence();
+            // (loads of several pieces in flight: a piece is a trip to L2, and this is the end of the CTA's work)
             float mm = -CUDART_INF_F, ll = 0.f;
-            for (int c = c0; c <= c1; ++c) mm = fmaxf(mm, __ldcg(pm + piece(c) * 128 + r).x);
-            const float mu = mm == -CUDART_INF_F ? 0.f : mm;
+#pragma unroll 4
             for (int c = c0; c <= c1; ++c) {
-                const float2 v = __ldcg(pm + piece(c) * 128 + r);
-                ll = fmaf(v.y, ex2(v.x - mu), ll);
+                const float2 x = __ldcg(pm + piece(c) * 128 + r);
+                const float m1 = fmaxf(mm, x.x), mu = m1 == -CUDART_INF_F ? 0.f : m1;
+                ll = fmaf(x.y, ex2(x.x - mu), ll * ex2(mm - mu));
+                mm = m1;
             }
+            const float mu = mm == -CUDART_INF_F ? 0.f : mm;
             const float inv = ll > 0.f ? 1.f / ll : 0.f;
 #pragma unroll 1
             for (int c = 0; c < kD; c += 32) {
                 float v[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] = 0.f;
+#pragma unroll 2
                 for (int p = c0; p <= c1; ++p) {
                     const size_t at = piece(p);
                     const float f = ex2(__ldcg(pm + at * 128 + r).x - mu);
-                    if (f == 0.f) continue;  // nothing summed there (the piece's O may be unwritten)
+                    float4 o[8];
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        const float4 o = __ldcg(po + (at * 32 + (c + j) / 4) * 128 + r);
-                        v[j] = fmaf(o.x, f, v[j]);
-                        v[j + 1] = fmaf(o.y, f, v[j + 1]);
-                        v[j + 2] = fmaf(o.z, f, v[j + 2]);
-                        v[j + 3] = fmaf(o.w, f, v[j + 3]);
+                    for (int j = 0; j < 8; ++j) o[j] = __ldcg(po + (at * 32 + c / 4 + j) * 128 + r);
+                    const bool none = f == 0.f;  // nothing summed there: the piece's O may be unwritten
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        v[4 * j] = none ? v[4 * j] : fmaf(o[j].x, f, v[4 * j]);
+                        v[4 * j + 1] = none ? v[4 * j + 1] : fmaf(o[j].y, f, v[4 * j + 1]);
+                        v[4 * j + 2] = none ? v[4 * j + 2] : fmaf(o[j].z, f, v[4 * j + 2]);
+                        v[4 * j + 3] = none ? v[4 * j + 3] : fmaf(o[j].w, f, v[4 * j + 3]);
                     }
                 }
                 store(c, v, inv);
