@@ -62,7 +62,7 @@ bool configure_chunk_attention_tile();
 
 // CUDA-core kernels: float32 models
 constexpr int kChunkSimtCtas = 2 * kChunkCtas;
-constexpr int kChunkSimtRows = 64;  // query vectors per unit
+constexpr int kChunkSimtRows = 64, kChunkSimtFew = 8;  // query vectors per unit of the two shapes
 template <typename T, int D> int launch_chunk_attention_simt(const ChunkAttnDev& a, int sms, cudaStream_t s);
 bool configure_chunk_attention_simt();
 

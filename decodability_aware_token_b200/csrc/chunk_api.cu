@@ -45,11 +45,11 @@ size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 // words: error word, plan arrivals, attention counters (all zero between calls)
 Layout plan_layout(const focus_chunk_cfg* c) {
     const size_t vecs = c->dtype == FOCUS_DTYPE_BF16 ? (size_t)2 * kChunkCtas * kChunkTileRows
-                                                     : (size_t)2 * kChunkSimtCtas * kChunkSimtRows;
+                                                     : (size_t)2 * kChunkSimtCtas * (kChunkSimtRows + kChunkSimtFew);
     Layout l{};
     l.freq = 0;
     l.words = align_up(l.freq + (size_t)c->head_dim / 2 * 8, 256);
-    l.part_ml = align_up(l.words + (2 + (size_t)kChunkSimtCtas) * 4, 256);
+    l.part_ml = align_up(l.words + (2 + (size_t)2 * kChunkSimtCtas) * 4, 256);
     l.part_o = align_up(l.part_ml + vecs * 2 * 4, 256);
     l.total = align_up(l.part_o + vecs * c->head_dim * 4, 256);
     return l;

@@ -8,7 +8,7 @@
 // once per group.  Two shapes: TR = 64 (chunks; 4 x (KEYS / 16) scores per thread, bound by the FMA pipe),
 // TR = 8 (8 query vectors or fewer: single tokens, short chunks).  Measured, 4/4 heads of 64, TR = 8 / TR = 64 for
 // single tokens over 512 to 2048 keys: 8 requests 21.7 / 34.8 us, 64 requests 63.9 / 165.7; 5 single tokens and 6
-// prompts of up to 401 tokens 53 us.  K and V of the next block are
+// prompts of up to 401 tokens 35 us.  K and V of the next block are
 // on their way while one is used (cp.async, two buffers).  The walk over the keys is split over the CTAs by
 // chunk_work.cuh.
 #include <math_constants.h>
@@ -19,7 +19,7 @@ namespace focus {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kFew = 8;  // query vectors of the few-row shape
+constexpr int kFew = kChunkSimtFew;
 
 template <int D, int TR> struct SimtShape {
     static constexpr int KEYS = D == 128 ? 32 : 64;
@@ -34,13 +34,11 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool ther
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
 }
 
-template <typename T, int D, int TR>
-__global__ void __launch_bounds__(kThreads, 2) chunk_attn_simt_kernel(ChunkAttnDev a) {
+template <typename T, int D, int TR> __device__ __forceinline__ void simt_walk(const ChunkAttnDev& a) {
     static_assert(sizeof(T) == 4, "copies move float32 rows as they are");
     using S = SimtShape<D, TR>;
     constexpr int KEYS = S::KEYS, KSTR = S::KSTR, PSTR = S::PSTR;
     constexpr bool kTile = TR == 64;
-    pdl_entry();
     extern __shared__ __align__(16) float smem[];
     float* qs = smem;                 // [TR][KSTR]
     float* ks = qs + S::Q_F;          // [2][KEYS][KSTR]
@@ -382,40 +380,58 @@ __global__ void __launch_bounds__(kThreads, 2) chunk_attn_simt_kernel(ChunkAttnD
     }
 }
 
+template <typename T, int D, int TR> __global__ void __launch_bounds__(kThreads, 2) chunk_attn_simt_kernel(ChunkAttnDev a) {
+    pdl_entry();
+    simt_walk<T, D, TR>(a);
+}
+
+// Both shapes in one launch: row 0 of the grid takes the requests of many query vectors, row 1 the others as its CTAs make
+// room, each with scratch of its own (5 single tokens and 6 chunks: 52 us as two launches, 35 us; 40 and 5 larger ones,
+// 8/8 heads of 128: 381 and 368).
+template <typename T, int D> __global__ void __launch_bounds__(kThreads, 2) chunk_attn_simt_both_kernel(ChunkAttnDev a) {
+    pdl_entry();
+    if (blockIdx.y == 0) {
+        simt_walk<T, D, 64>(a);
+    } else {
+        a.part_o += (size_t)2 * kChunkSimtCtas * kChunkSimtRows * D;
+        a.part_ml += (size_t)2 * kChunkSimtCtas * kChunkSimtRows * 2;
+        a.counters += kChunkSimtCtas;
+        simt_walk<T, D, kFew>(a);
+    }
+}
+
 // dynamic shared memory: the tiles, or the schedule's sums if there are very many requests
 template <int D, int TR> int simt_smem(int N) {
     const int sched = (N + 1) * 8;
     return SimtShape<D, TR>::SMEM > sched ? SimtShape<D, TR>::SMEM : sched;
 }
 
-template <typename T, int D, int TR> bool configure_one() {
-    return cudaFuncSetAttribute(chunk_attn_simt_kernel<T, D, TR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                simt_smem<D, TR>(kChunkMaxRequests)) == cudaSuccess &&
-           max_shared_carveout((const void*)chunk_attn_simt_kernel<T, D, TR>);
+template <int D> int simt_smem_both(int N) {
+    return simt_smem<D, 64>(N) > simt_smem<D, kFew>(N) ? simt_smem<D, 64>(N) : simt_smem<D, kFew>(N);
+}
+
+bool configure_one(const void* kernel, int smem) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess &&
+           max_shared_carveout(kernel);
+}
+template <int D> bool configure_all() {
+    return configure_one((const void*)chunk_attn_simt_kernel<float, D, kFew>, simt_smem<D, kFew>(kChunkMaxRequests)) &&
+           configure_one((const void*)chunk_attn_simt_kernel<float, D, 64>, simt_smem<D, 64>(kChunkMaxRequests)) &&
+           configure_one((const void*)chunk_attn_simt_both_kernel<float, D>, simt_smem_both<D>(kChunkMaxRequests));
 }
 
 }  // namespace
 
-bool configure_chunk_attention_simt() {
-    return configure_one<float, 64, 8>() && configure_one<float, 64, 64>() && configure_one<float, 128, 8>() &&
-           configure_one<float, 128, 64>();
-}
+bool configure_chunk_attention_simt() { return configure_all<64>() && configure_all<128>(); }
 
 template <typename T, int D> int launch_chunk_attention_simt(const ChunkAttnDev& a, int sms, cudaStream_t s) {
-    const dim3 grid(2 * sms < kChunkSimtCtas ? 2 * sms : kChunkSimtCtas), block(kThreads);
-    int n = 0;
-    const long long most = (long long)a.max_new * a.G;
-    if (most > kFew) {  // units of 64 query vectors
-        if (launched(launch_pdl(chunk_attn_simt_kernel<T, D, 64>, grid, block, simt_smem<D, 64>(a.N), s, 0, a)) < 0)
-            return -1;
-        ++n;
-    }
-    if (a.G <= kFew) {
-        if (launched(launch_pdl(chunk_attn_simt_kernel<T, D, 8>, grid, block, simt_smem<D, 8>(a.N), s, 0, a)) < 0)
-            return -1;
-        ++n;
-    }
-    return n;
+    const dim3 block(kThreads);
+    const unsigned ctas = 2 * sms < kChunkSimtCtas ? 2 * sms : kChunkSimtCtas;
+    const bool many = (long long)a.max_new * a.G > kFew, few = a.G <= kFew;   // shapes that requests may need
+    if (many && few)
+        return launched(launch_pdl(chunk_attn_simt_both_kernel<T, D>, dim3(ctas, 2), block, simt_smem_both<D>(a.N), s, 0, a));
+    if (many) return launched(launch_pdl(chunk_attn_simt_kernel<T, D, 64>, dim3(ctas), block, simt_smem<D, 64>(a.N), s, 0, a));
+    return launched(launch_pdl(chunk_attn_simt_kernel<T, D, kFew>, dim3(ctas), block, simt_smem<D, kFew>(a.N), s, 0, a));
 }
 
 template int launch_chunk_attention_simt<float, 64>(const ChunkAttnDev&, int, cudaStream_t);
