@@ -39,10 +39,10 @@ struct ChunkAttnDev {
     long long q_stride, out_stride;  // elements
     int N, rows, max_new, Hq, Hkv, G, L, layer, S, n_pages, max_pages, mask_block;
     float scale;
-    bool more;        // bf16: the tile kernel follows the few-row kernel and may be launched at once.  Otherwise nothing is
-                      // launched before the work is handed out: the next operator's CTAs, waiting on the SMs, cost more
-                      // than their early launch gives (norm and rotation, then attention, repeated: 32 single tokens
-                      // 26.0 -> 23.8 us, 8192-token prompt 373 -> 360)
+    // bf16: the few-row and the tile kernel both run in this call.  They share nothing, so the tile kernel does not wait for
+    // the other one: its CTAs start as the SMs come free, and it only waits at its end, so that who waits for it
+    // has waited for both (40 single tokens and 8 chunks: 308 -> 292 us).
+    bool pair;
     bool small_walk;  // the launch's key blocks, and their products with the CTA count, fit 31 bits
     // scratch of units whose key walk is split over CTAs: slot 2c / 2c + 1 is CTA c's first / last piece
     float* part_o;

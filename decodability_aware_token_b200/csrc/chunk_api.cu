@@ -44,7 +44,7 @@ size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 // words: error word, plan arrivals, attention counters (all zero between calls)
 Layout plan_layout(const focus_chunk_cfg* c) {
-    const size_t vecs = c->dtype == FOCUS_DTYPE_BF16 ? (size_t)2 * kChunkCtas * kChunkTileRows
+    const size_t vecs = c->dtype == FOCUS_DTYPE_BF16 ? (size_t)2 * kChunkCtas * (kChunkTileRows + kChunkFewRows)
                                                      : (size_t)2 * kChunkSimtCtas * (kChunkSimtRows + kChunkSimtFew);
     Layout l{};
     l.freq = 0;
@@ -261,9 +261,13 @@ int focus_chunk_attention(focus_chunk_ctx* c, const focus_chunk_attn* p, void* s
     if (bf) {
         // each kernel serves the requests on its side of kChunkFewRows query vectors and skips the others
         const bool tile = (int64_t)a.max_new * a.G > kChunkFewRows;
-        ChunkAttnDev few = a;
-        few.more = tile;
-        n = a.G <= kChunkFewRows ? launch_chunk_attention_few(few, c->sms, s) : 0;
+        const bool few = a.G <= kChunkFewRows;
+        a.pair = few && tile;
+        ChunkAttnDev f = a;
+        f.part_o += (size_t)2 * kChunkCtas * kChunkTileRows * c->cfg.head_dim;
+        f.part_ml += (size_t)2 * kChunkCtas * kChunkTileRows * 2;
+        f.counters += 2 * kChunkCtas;
+        n = few ? launch_chunk_attention_few(f, c->sms, s) : 0;
         if (n >= 0 && tile) n = launch_chunk_attention_tile(a, c->sms, s);
     } else {
         n = c->cfg.head_dim == 64 ? launch_chunk_attention_simt<float, 64>(a, c->sms, s)

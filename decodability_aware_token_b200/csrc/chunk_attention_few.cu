@@ -72,7 +72,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 __global__ void __launch_bounds__(kFewThreads, 1)
 chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev a) {
-    if (a.more) pdl_trigger();
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float* join = reinterpret_cast<float*>(ring + kStages * kStage);  // [warp][2 rows][128]
@@ -102,6 +101,7 @@ chunk_attn_few_kernel(const __grid_constant__ CUtensorMap pool_map, ChunkAttnDev
         asm volatile("prefetch.tensormap [%0];" ::"l"(&pool_map) : "memory");
     }
     pdl_wait();
+    if (a.pair) pdl_trigger();  // (behind the wait: the tile kernel may rely on it)
     const ChunkShape sh{kRows / a.G, 0, kRows};
     chunk_schedule<kKeys, 2>(a, sh, reinterpret_cast<long long*>(ring), red, &rg);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the ring held the schedule's sums

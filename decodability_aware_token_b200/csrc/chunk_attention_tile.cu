@@ -246,7 +246,7 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    pdl_wait();
+    if (!a.pair) pdl_wait();
 
     const int tpt = 128 / a.G;  // tokens per tile
     // The copies leave the query rows past G tokens' heads alone; whatever is there would send its warp through the
@@ -679,6 +679,7 @@ chunk_attn_tile_kernel(const __grid_constant__ CUtensorMap pool_map, const __gri
             }
         }
     }
+    if (a.pair) pdl_wait();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

@@ -112,7 +112,7 @@ struct PageWalk {
     __device__ __forceinline__ void load() {
         const int i = at + (int)(threadIdx.x & 31);
         ahead0 = at;
-        ahead = i < max_pages ? pt[i] : -1;
+        ahead = i < max_pages ? __ldcg(pt + i) : -1;
     }
     // Lane p < ppb gets the id of the block's page p, -1 if there is none (`got` false) or it is not in the pool;
     // `bad` (every lane): the block's 16-key groups that a bad id covers; returns the number of good pages.

@@ -19,12 +19,13 @@ struct ChunkReq {
     int row0, n, kv;  // first row, rows, cached keys (n = 0: nothing to do)
 };
 
-// Request b's rows and keys; a request whose numbers are out of range is flagged and skipped.
+// Request b's rows and keys; a request whose numbers are out of range is flagged and skipped.  (Read from L2: a kernel
+// that does not wait for the one before it must not meet an old line.)
 __device__ __forceinline__ ChunkReq chunk_req(const ChunkAttnDev& a, int b, bool flag) {
     ChunkReq r;
-    r.row0 = a.row_offsets[b];
-    const int end = a.row_offsets[b + 1];
-    r.kv = a.kv_len[b];
+    r.row0 = __ldcg(a.row_offsets + b);
+    const int end = __ldcg(a.row_offsets + b + 1);
+    r.kv = __ldcg(a.kv_len + b);
     r.n = 0;
     if (r.row0 < 0 || end < r.row0 || end > a.rows || end - r.row0 > a.max_new) {
         if (flag) raise_err(a.err, FOCUS_DEVERR_ROWS);
