@@ -47,7 +47,8 @@ struct ChunkAttnDev {
     // scratch of units whose key walk is split over CTAs: slot 2c / 2c + 1 is CTA c's first / last piece
     float* part_o;
     float* part_ml;
-    int* counters;   // [kChunkCtas] arrivals at the unit whose first piece is CTA c's; zero between launches
+    int* counters;   // arrivals at the unit (tile kernel: at each of its two tiles) whose first piece is CTA c's; zero
+                     // between launches
     int* err;
 };
 // bf16 models: requests of at most kChunkFewRows query vectors per KV head (single tokens) go to one kernel, the others
