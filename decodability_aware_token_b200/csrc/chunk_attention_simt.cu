@@ -26,7 +26,7 @@ template <int D, int TR> struct SimtShape {
     static constexpr int KSTR = D + 4;      // padded rows: 16 keys' float4 fall on distinct banks
     static constexpr int PSTR = KEYS + 4;
     static constexpr int Q_F = TR * KSTR, K_F = KEYS * KSTR, V_F = KEYS * D, P_F = TR * PSTR;
-    static constexpr int SMEM = (Q_F + 2 * (K_F + V_F) + P_F + 4 * TR) * 4 + 2 * KEYS * 8;
+    static constexpr int SMEM = (Q_F + 2 * (K_F + V_F) + P_F + 4 * TR) * 4 + 3 * KEYS * 8;
 };
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool there) {
@@ -48,7 +48,9 @@ template <typename T, int D, int TR> __device__ __forceinline__ void simt_walk(c
     float* ls = ms + TR;              // [TR] denominators
     float* al = ls + TR;              // [TR] rescale factors of the block; a piece's weight at the end
     int* vis = reinterpret_cast<int*>(al + TR);                  // [TR] visible keys of each row
-    long long* row_at = reinterpret_cast<long long*>(vis + TR);  // [2][KEYS] element offset of the key's row, -1: none
+    // [3][KEYS] element offset of the key's row, -1: none.  Three blocks' worth: a warp that is done with block b - 1
+    // writes block b + 1's while others still read block b - 1's, and block b's are for its copies.
+    long long* row_at = reinterpret_cast<long long*>(vis + TR);
     __shared__ ChunkRange rg;
     __shared__ long long red[32];
     __shared__ int last_s;
@@ -80,14 +82,14 @@ template <typename T, int D, int TR> __device__ __forceinline__ void simt_walk(c
                 else
                     raise_err(a.err, FOCUS_DEVERR_PAGE_ID);
             }
-            row_at[(blk & 1) * KEYS + tid] = at;
+            row_at[blk % 3 * KEYS + tid] = at;
         };
         auto copy = [&](int blk) {
             float *kd = ks + (blk & 1) * S::K_F, *vd = vs + (blk & 1) * S::V_F;
 #pragma unroll
             for (int i = tid; i < KEYS * (D / 4); i += kThreads) {
                 const int j = i / (D / 4), c = (i - j * (D / 4)) * 4;
-                const long long at = row_at[(blk & 1) * KEYS + j];
+                const long long at = row_at[blk % 3 * KEYS + j];
                 const T* src = pool + (at < 0 ? 0 : at) + c;
                 cp_async16(kd + j * KSTR + c, src, at >= 0);
                 cp_async16(vd + j * D + c, at < 0 ? src : src + v_off, at >= 0);
@@ -132,7 +134,7 @@ template <typename T, int D, int TR> __device__ __forceinline__ void simt_walk(c
             __syncthreads();  // this block has landed, the one before has been read
             if (b + 1 < nb) copy(blk + 1);
             const float *kb = ks + (blk & 1) * S::K_F, *vb = vs + (blk & 1) * S::V_F;
-            const long long* there = row_at + (blk & 1) * KEYS;
+            const long long* there = row_at + blk % 3 * KEYS;
             if constexpr (kTile) {
                 constexpr int KPT = KEYS / 16;
                 const int ty = tid >> 4, tx = tid & 15;
