@@ -6,6 +6,7 @@ missing, importing the step API raises ImportError: there is no fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import dataclasses
 import math
@@ -38,6 +39,12 @@ def _check(rc: int, where: str):
 
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else C.c_void_p(t.data_ptr())
+
+
+def _under(stream: Optional[torch.cuda.Stream]):
+    """Where a call allocates what it is not given: on the stream its kernels run on, so that fills come before them and
+    memory that is freed is not handed out while they run."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _need(t: torch.Tensor, name: str, dtype, device, shape=None):
@@ -240,7 +247,7 @@ class FocusContext:
         pool = batch["kv_pool"]
         n_pages, page_size, pool_ptr = chunk._pool(pool, 0)
         packed, out = chunk._plan_args(batch["prefix_len"], new_len, batch["page_table"], free_pages, free_head, page_size,
-                                       n_pages, max_rows, out)
+                                       n_pages, max_rows, out, stream)
         plan = _abi.ChunkPlanArgs.from_buffer_copy(packed)
         if tokens.dim() != 2 or tokens.shape[0] != plan.n_requests:
             raise ValueError(f"tokens: shape {tuple(tokens.shape)}, expected [{plan.n_requests}, max_new]")

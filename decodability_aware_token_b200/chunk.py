@@ -13,7 +13,7 @@ from typing import Optional
 
 import torch
 
-from . import _abi, _check, _need
+from . import _abi, _check, _need, _under
 
 __all__ = ["ChunkContext", "ChunkPlan"]
 
@@ -38,8 +38,9 @@ class ChunkContext:
     """The chunk operators of one model geometry: scratch, rotary frequencies and a device error word.
 
     Calls are asynchronous on `stream` (default: torch's current stream on the context's device), allocate
-    only the outputs they are not given, and can be captured in CUDA graphs.  Two calls of one context must
-    not overlap in time; use a context per concurrent stream.
+    only the outputs they are not given, and can be captured in CUDA graphs.  Outputs are allocated on that stream: a
+    consumer on another one waits for it, as for any tensor made under torch.cuda.stream.  Two calls of one
+    context must not overlap in time; use a context per concurrent stream.
     """
     _marshal = None
 
@@ -163,16 +164,19 @@ class ChunkContext:
                 return out
             if rc is not None:
                 _check(rc, where)
-        args, out = self._plan_args(prefix_len, new_len, page_table, free_pages, free_head, page_size, n_pages, max_rows, out)
+        args, out = self._plan_args(prefix_len, new_len, page_table, free_pages, free_head, page_size, n_pages, max_rows, out,
+                                    stream)
         self._call(0, args, where, stream)
         return out
 
-    def _plan_args(self, prefix_len, new_len, page_table, free_pages, free_head, page_size, n_pages, max_rows, out):
+    def _plan_args(self, prefix_len, new_len, page_table, free_pages, free_head, page_size, n_pages, max_rows, out,
+                   stream=None):
         n = prefix_len.shape[0]
         if out is None:
             if max_rows is None:
                 raise ValueError("plan: give max_rows or out")
-            out = self.alloc_plan(n, max_rows)
+            with _under(stream):
+                out = self.alloc_plan(n, max_rows)
         rows = out.row_req.shape[0]
         if max_rows is not None and max_rows != rows:
             raise ValueError(f"plan: out holds {rows} rows, max_rows is {max_rows}")
@@ -205,7 +209,8 @@ class ChunkContext:
         kp, ks = self._heads(k, "k", rows, hkv)
         vp, vs = self._heads(v, "v", rows, hkv)
         if out is None:
-            out = torch.zeros(rows, hq, self.head_dim, dtype=self.dtype, device=self.device)
+            with _under(stream):
+                out = torch.zeros(rows, hq, self.head_dim, dtype=self.dtype, device=self.device)
         op, os_ = self._heads(out, "out", rows, hq)
         n_pages, page_size, pool = self._pool(kv_pool, layer)
         gq = self._gain(q_norm, "q_norm") if q_norm is not None else 0
@@ -244,7 +249,8 @@ class ChunkContext:
         rows, n, hq = q.shape[0], kv_len.shape[0], self.n_q_heads
         qp, qs = self._heads(q, "q", rows, hq)
         if out is None:
-            out = torch.zeros(rows, hq, self.head_dim, dtype=self.dtype, device=self.device)
+            with _under(stream):
+                out = torch.zeros(rows, hq, self.head_dim, dtype=self.dtype, device=self.device)
         op, os_ = self._heads(out, "out", rows, hq)
         n_pages, page_size, pool = self._pool(kv_pool, layer)
         if max_new is None:

@@ -3,7 +3,7 @@ and the tolerances are those of test_gpu_chunk.py."""
 import pytest
 import torch
 
-from test_gpu_chunk import F32, Batch, _ctx
+from test_gpu_chunk import BF, F32, Batch, _ctx, _i32
 
 pytestmark = pytest.mark.gpu
 
@@ -28,3 +28,51 @@ def test_float32_walks_of_many_blocks_repeat_themselves(d, S):
         outs = [b.run(ctx) for _ in range(60)]
         torch.cuda.synchronize()
         assert all(torch.equal(o, first) for o in outs)
+
+
+def _keep_busy():
+    """Some tens of milliseconds of products on the current stream."""
+    a = torch.ones(8192, 8192, device="cuda", dtype=BF)
+    for _ in range(60):
+        a = torch.matmul(a, a).mul_(2.0 ** -13)
+    return a
+
+
+@pytest.mark.parametrize("native", [True, False])
+def test_outputs_a_call_allocates_for_a_side_stream_are_ordered_with_it(native):
+    """No `out`, a stream of its own and a current stream that is far behind: nothing of the call, the zero fill of its
+    outputs included, may be queued on the current stream."""
+    b = Batch([(1, 90), (40, 200), (3, 3)], 8, 2, 128, BF, 16, seed=4, pad=3)
+    k, v = (torch.randn(b.T, 2, 128, device="cuda").to(BF) for _ in range(2))
+    prefix, new, free, head = _i32([0, 5, 9]), _i32([7, 0, 20]), torch.arange(8, dtype=torch.int32, device="cuda"), _i32([0])
+    with _ctx(8, 2, 128, BF, n=3, pages=b.max_pages) as ctx:
+        if not native:
+            ctx._marshal = None
+
+        def calls(**kw):
+            table = b.table.clone() if not kw else tables
+            p = ctx.plan(prefix, new, table, free, head, page_size=16, n_pages=b.pool.shape[0], max_rows=33, **kw)
+            pool = b.pool.clone() if not kw else pools
+            q = ctx.qk_norm_rope(b.q, k, v, pool, 0, p_rows, p_slots, **kw)
+            return [p.row_offsets, p.kv_len, p.row_req, p.row_pos, p.row_slot, p.free_next, q, b.run(ctx, **kw)]
+
+        p_rows, p_slots = torch.arange(b.T, dtype=torch.int32, device="cuda"), torch.full((b.T,), -1, dtype=torch.int32, device="cuda")
+        tables, pools = b.table.clone(), b.pool.clone()
+        want = calls()
+        busy = _keep_busy()                                     # (loads the products' kernels)
+        side = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        for _ in range(3):
+            busy = _keep_busy()
+            late = torch.cuda.Event()
+            late.record()
+            got = calls(stream=side)
+            side.synchronize()
+            assert not late.query()                             # the current stream is behind: the calls did not wait for it
+            with torch.cuda.stream(side):
+                seen = [t.cpu() for t in got]
+            torch.cuda.synchronize()
+            after = [t.cpu() for t in got]
+            for w, s, a in zip(want, seen, after):
+                assert torch.equal(s, w.cpu()) and torch.equal(a, w.cpu())
+        assert ctx.device_error() == (0, 0) and bool(torch.isfinite(busy.float()).all())
