@@ -199,7 +199,8 @@ class FocusContext:
         """Enqueue one focused step on `stream` (default: torch's current stream). Asynchronous."""
         N, B = batch["block_tokens"].shape
         if out is None:
-            out = self.alloc_outputs(N, B)
+            with _under(stream):
+                out = self.alloc_outputs(N, B)
         cb, cp, co = self._marshal(batch, params, out)
         with torch.cuda.device(self.device):
             s = stream if stream is not None else torch.cuda.current_stream(self.device)
@@ -222,7 +223,8 @@ class FocusContext:
         returns (outputs of the last call, number of decoding steps).  Synchronises after every step."""
         N, B = batch["block_tokens"].shape
         if out is None:
-            out = self.alloc_outputs(N, B)
+            with _under(stream):
+                out = self.alloc_outputs(N, B)
         cb, cp, co = self._marshal(batch, params, out)
         steps = C.c_int32(0)
         with torch.cuda.device(self.device):

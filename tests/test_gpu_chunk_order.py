@@ -30,10 +30,10 @@ def test_float32_walks_of_many_blocks_repeat_themselves(d, S):
         assert all(torch.equal(o, first) for o in outs)
 
 
-def _keep_busy():
-    """Some tens of milliseconds of products on the current stream."""
+def _keep_busy(products=60):
+    """Work on the current stream, about 0.7 ms a product."""
     a = torch.ones(8192, 8192, device="cuda", dtype=BF)
-    for _ in range(60):
+    for _ in range(products):
         a = torch.matmul(a, a).mul_(2.0 ** -13)
     return a
 
@@ -76,3 +76,40 @@ def test_outputs_a_call_allocates_for_a_side_stream_are_ordered_with_it(native):
             for w, s, a in zip(want, seen, after):
                 assert torch.equal(s, w.cpu()) and torch.equal(a, w.cpu())
         assert ctx.device_error() == (0, 0) and bool(torch.isfinite(busy.float()).all())
+
+
+@pytest.mark.parametrize("name", ["tiny", "small_bf16"])
+@pytest.mark.parametrize("call", ["step", "decode_block"])
+def test_outputs_a_step_allocates_for_a_side_stream_are_ordered_with_it(name, call):
+    import focus_synth as fs
+    from decodability_aware_token_b200 import FocusContext, StepParams
+    from gpu_harness import limits_for, step_params, to_device
+    case = fs.make_case(name)
+    params = step_params(case.work)
+    lim = limits_for(case, params)
+    lim["max_keep"] = case.work.block                            # (decode_block's dense calls keep every position)
+    with FocusContext(case.shape, to_device(case), **lim) as ctx:
+        run, sp = getattr(ctx, call), StepParams(**params)
+        batch = lambda: {k: v.cuda().clone() for k, v in case.batch.items()}
+        outputs = lambda r: (r if call == "step" else r[0]).tensors()
+        first = outputs(run(batch(), sp))
+        torch.cuda.synchronize()
+        want, flags = {k: t.cpu() for k, t in first.items()}, ctx.device_error()
+        # (the case's page table ends with the prefix: a decoded block has no page to be committed to)
+        assert flags[1] in ((0,) if call == "step" else (0, 0x2, 0x4))
+        del first
+        _keep_busy()
+        side = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        b = batch()
+        torch.cuda.synchronize()
+        busy = _keep_busy(60 if call == "step" else 900)       # (a block is a few dozen steps, each read by the host)
+        late = torch.cuda.Event()
+        late.record()
+        got = outputs(run(b, sp, stream=side))
+        side.synchronize()
+        assert not late.query()
+        torch.cuda.synchronize()
+        assert ctx.device_error() == flags and bool(torch.isfinite(busy.float()).all())
+        for k, t in got.items():
+            assert torch.equal(t.cpu(), want[k]), k
