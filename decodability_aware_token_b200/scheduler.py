@@ -35,6 +35,7 @@ attention splits long key walks into pieces only when a batch has few (request, 
 """
 from __future__ import annotations
 
+import contextlib
 import dataclasses
 from typing import Dict, List, Optional
 
@@ -80,7 +81,11 @@ class IterationStats:
 
 
 class FocusEngine:
-    """Runs the scheduler's calls on the GPU through a FocusContext (steps and commits on slot views)."""
+    """Runs the scheduler's calls on the GPU through a FocusContext (steps and commits on slot views).
+
+    The calls run on `stream` (default: torch's current stream).  With a stream of its own a call starts behind what
+    the current stream holds and the current stream goes on behind the call: the caller reads and writes the views
+    between calls, and may drop a call's arguments as soon as it returns."""
 
     def __init__(self, ctx, params, stream: Optional[torch.cuda.Stream] = None, chunk=None, mask_block: int = 1):
         """`chunk`: a ChunkContext of the model's geometry, needed for requests that bring prompt tokens;
@@ -91,6 +96,20 @@ class FocusEngine:
         self.dense = dataclasses.replace(self.focused, forced_keep_frac=1.0)
         self.stream = stream
         self._out = None
+
+    @contextlib.contextmanager
+    def _ordered(self):
+        """The body's work, allocations included, on the engine's stream, between what the current one did and will do."""
+        here = None if self.stream is None else torch.cuda.current_stream(self.stream.device)
+        if here is None or here == self.stream:
+            yield
+            return
+        self.stream.wait_stream(here)
+        try:
+            with torch.cuda.stream(self.stream):
+                yield
+        finally:
+            here.wait_stream(self.stream)
 
     def capacity_check(self, slots: int, block: int) -> None:
         """The context must take every slot in one call and keep all B positions in the dense steps."""
@@ -109,10 +128,12 @@ class FocusEngine:
 
     def step(self, view: Dict[str, torch.Tensor], dense: bool) -> None:
         n, block = view["block_tokens"].shape
-        self.ctx.step(view, self.dense if dense else self.focused, out=self._outputs(n, block), stream=self.stream)
+        with self._ordered():
+            self.ctx.step(view, self.dense if dense else self.focused, out=self._outputs(n, block), stream=self.stream)
 
     def commit(self, view: Dict[str, torch.Tensor]) -> None:
-        self.ctx.commit_block(view, stream=self.stream)
+        with self._ordered():
+            self.ctx.commit_block(view, stream=self.stream)
 
     def prefill_rows(self) -> int:
         """Prompt tokens one call takes (0: no prompts)."""
@@ -121,8 +142,9 @@ class FocusEngine:
     def prefill(self, view: Dict[str, torch.Tensor], tokens: torch.Tensor, new_len: torch.Tensor,
                 pages: torch.Tensor) -> None:
         """Run a chunk of the view's prompts; its new pages are `pages`, in request order."""
-        head = torch.zeros(1, dtype=torch.int32, device=tokens.device)
-        self.ctx.prefill(self.chunk, tokens, new_len, view, pages, head, mask_block=self.mask_block, stream=self.stream)
+        with self._ordered():
+            head = torch.zeros(1, dtype=torch.int32, device=tokens.device)
+            self.ctx.prefill(self.chunk, tokens, new_len, view, pages, head, mask_block=self.mask_block, stream=self.stream)
 
 
 class EffectiveBatchScheduler:

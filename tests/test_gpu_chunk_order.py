@@ -113,3 +113,76 @@ def test_outputs_a_step_allocates_for_a_side_stream_are_ordered_with_it(name, ca
         assert ctx.device_error() == flags and bool(torch.isfinite(busy.float()).all())
         for k, t in got.items():
             assert torch.equal(t.cpu(), want[k]), k
+
+
+@pytest.mark.parametrize("S", [16, 64])
+def test_an_engine_on_its_own_stream_prefills_what_the_current_stream_prepared(S):
+    """The caller's tensors are written late on the current stream, dropped when the call returns, and their memory
+    is written again at once."""
+    import focus_synth as fs
+    from decodability_aware_token_b200 import ChunkContext, FocusContext, StepParams
+    from decodability_aware_token_b200.scheduler import FocusEngine
+    from gpu_harness import to_device
+    case = fs.make_case("small_bf16")
+    s, lens = case.shape, [37, 64, 5, 100]
+    N, mp = len(lens), 8
+    g = torch.Generator().manual_seed(8)
+    host = torch.randint(0, s.vocab, (N, max(lens)), generator=g, dtype=torch.int32)
+    need = [-(-n // S) for n in lens]
+    with FocusContext(s, to_device(case), max_requests=8, max_block=64, max_keep=64, max_pages_per_req=mp) as ctx, \
+            ChunkContext(n_layers=s.n_layers, n_q_heads=s.n_q_heads, n_kv_heads=s.n_kv_heads, head_dim=s.head_dim,
+                         max_requests=N, max_pages_per_req=mp, rope_theta=s.rope_theta) as chunk:
+        def run(stream):
+            eng = FocusEngine(ctx, StepParams(), stream=stream, chunk=chunk)
+            pool = torch.zeros(sum(need) + 1, s.n_layers, 2, s.n_kv_heads, S, s.head_dim, dtype=BF, device="cuda")
+            view = dict(prefix_len=torch.full((N,), 3, dtype=torch.int32, device="cuda"), kv_pool=pool,
+                        page_table=torch.full((N, mp), -1, dtype=torch.int32, device="cuda"))
+            ids = [x.cuda() for x in (host, torch.tensor(lens, dtype=torch.int32), torch.arange(sum(need), dtype=torch.int32))]
+            torch.cuda.synchronize()
+            if stream is not None:
+                _keep_busy()
+            view["prefix_len"].zero_()
+            args = [torch.empty_like(x).copy_(x) for x in ids]
+            eng.prefill(view, *args)
+            shapes = [a.shape for a in args]
+            del args
+            trash = [torch.full(sh, 7, dtype=torch.int32, device="cuda") for sh in shapes for _ in range(3)]
+            got = (view["prefix_len"].tolist(), view["page_table"].cpu(), pool.cpu())   # (read on the current stream)
+            assert ctx.device_error() == (0, 0) and chunk.device_error() == (0, 0) and len(trash) == 9
+            return got
+        want = run(None)
+        assert want[0] == lens
+        for _ in range(3):
+            got = run(torch.cuda.Stream())
+            assert got[0] == want[0] and torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+
+
+def test_the_scheduler_with_an_engine_on_its_own_stream():
+    import focus_synth as fs
+    from decodability_aware_token_b200 import ChunkContext, FocusContext, StepParams
+    from decodability_aware_token_b200.scheduler import EffectiveBatchScheduler, FocusEngine, Request
+    from gpu_harness import to_device
+    case = fs.make_case("small_bf16", k_min=1, k_max=4)
+    s, w, model = case.shape, case.work, to_device(case)
+    B, S, mp, slots = 16, 16, 10, 4
+    g = torch.Generator().manual_seed(19)
+    prompts = [torch.randint(0, s.vocab, (n,), generator=g).tolist() for n in (37, 1, 90, 20, 5)]
+
+    def run(stream):
+        pool = torch.zeros(60, s.n_layers, 2, s.n_kv_heads, S, s.head_dim, dtype=BF, device="cuda")
+        with FocusContext(s, model, max_requests=slots, max_block=B, max_keep=B, max_pages_per_req=mp) as ctx, \
+                ChunkContext(n_layers=s.n_layers, n_q_heads=s.n_q_heads, n_kv_heads=s.n_kv_heads, head_dim=s.head_dim,
+                             max_requests=slots, max_pages_per_req=mp, rope_theta=s.rope_theta) as chunk:
+            eng = FocusEngine(ctx, StepParams(w.tau, w.k_min, w.k_max, w.conf_threshold, w.alpha), stream=stream, chunk=chunk,
+                              mask_block=B)
+            sch = EffectiveBatchScheduler(eng, slots=slots, block=B, n_layers=s.n_layers, n_kv_heads=s.n_kv_heads,
+                                          head_dim=s.head_dim, max_pages_per_req=mp, kv_pool=pool, free_pages=list(range(60)),
+                                          mask_token=s.vocab - 1, k_max=w.k_max, keep_pages=True)
+            for r, toks in enumerate(prompts):
+                sch.submit(Request(r, r, len(toks), [], 2, prompt_tokens=toks))
+            res = sch.run(max_iterations=500)
+            assert ctx.device_error() == (0, 0) and chunk.device_error() == (0, 0)
+            return {r: ([b.tolist() for b in x.blocks], x.steps, x.pages) for r, x in res.items()}, pool.cpu()
+    want, pool = run(None)
+    got, pool2 = run(torch.cuda.Stream())
+    assert got == want and torch.equal(pool, pool2)
