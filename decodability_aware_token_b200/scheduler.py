@@ -141,10 +141,27 @@ class FocusEngine:
 
     def prefill(self, view: Dict[str, torch.Tensor], tokens: torch.Tensor, new_len: torch.Tensor,
                 pages: torch.Tensor) -> None:
-        """Run a chunk of the view's prompts; its new pages are `pages`, in request order."""
+        """Run a chunk of the view's prompts; its new pages are `pages`, in request order.  Arguments on the host are
+        copied.  Lengths on the host also tell how many rows the model has to run on; with lengths on the device every
+        entry of `tokens` counts as one."""
+        rows = int(new_len.sum()) if new_len.device.type == "cpu" else None
+        dev = view["prefix_len"].device
         with self._ordered():
-            head = torch.zeros(1, dtype=torch.int32, device=tokens.device)
-            self.ctx.prefill(self.chunk, tokens, new_len, view, pages, head, mask_block=self.mask_block, stream=self.stream)
+            head = torch.zeros(1, dtype=torch.int32, device=dev)
+            self.ctx.prefill(self.chunk, tokens.to(dev), new_len.to(dev), view, pages.to(dev), head, max_rows=rows,
+                             mask_block=self.mask_block, stream=self.stream)
+
+
+def share_rows(left: List[int], rows: int, step: int) -> List[int]:
+    """How many of `rows` each of the prompts with `left` tokens to go gets in one call: an equal part of what the shorter
+    ones leave, whole blocks of `step` unless it ends the prompt."""
+    take = [0] * len(left)
+    order = sorted((i for i, n in enumerate(left) if n > 0), key=lambda i: (left[i], i))
+    for at, i in enumerate(order):
+        part = rows // (len(order) - at)
+        take[i] = left[i] if left[i] <= part else part // step * step
+        rows -= take[i]
+    return take
 
 
 class EffectiveBatchScheduler:
@@ -258,31 +275,28 @@ class EffectiveBatchScheduler:
             self._prefill(fresh)
 
     def _prefill(self, slots: List[int]) -> None:
-        """Run the prompts of these (consecutive) slots through the model, several requests' chunks per call.  A chunk
-        ends at the prompt's end or at a multiple of the mask's block, whose positions see one another."""
-        rows, step = self.engine.prefill_rows(), self.engine.mask_block
-        S, dev = self.page_size, self.tokens.device
+        """Run the prompts of these slots through the model, several requests' chunks per call.  A chunk ends at the
+        prompt's end or at a multiple of the mask's block, whose positions see one another."""
+        rows, step, S = self.engine.prefill_rows(), self.engine.mask_block, self.page_size
         i32 = dict(dtype=torch.int32)
-        for at in range(0, len(slots), max(1, rows // step)):
-            group = slots[at:at + max(1, rows // step)]
-            a, b = group[0], group[-1] + 1
-            view = self._view(a, b)
-            per = rows // len(group) // step * step
-            prompts = {i: self.slot_req[i]["req"].prompt_tokens for i in group}
-            for i in group:
-                self.prefix_len[i] = 0
-            done = 0
-            while any(len(p) > done for p in prompts.values()):
-                width = min(per, max(len(p) for p in prompts.values()) - done)
-                tokens, new, pages = torch.zeros(b - a, width, **i32), torch.zeros(b - a, **i32), []
-                for i, p in prompts.items():
-                    part = p[done:done + width]
-                    tokens[i - a, : len(part)] = torch.tensor(part, **i32)
-                    new[i - a] = len(part)
-                    if part:
-                        pages += self.slot_req[i]["pages"][-(-done // S):-(-(done + len(part)) // S)]
-                self.engine.prefill(view, tokens.to(dev), new.to(dev), torch.tensor(pages, **i32).to(dev))
-                done += width
+        a, b = slots[0], slots[-1] + 1
+        view = self._view(a, b)
+        prompts = [self.slot_req[i]["req"].prompt_tokens for i in slots]
+        for i in slots:
+            self.prefix_len[i] = 0
+        done = [0] * len(slots)
+        while any(len(p) > d for p, d in zip(prompts, done)):
+            take = share_rows([len(p) - d for p, d in zip(prompts, done)], rows, step)
+            tokens, new, pages = torch.zeros(b - a, max(take), **i32), torch.zeros(b - a, **i32), []
+            for at, (i, p, n) in enumerate(zip(slots, prompts, take)):
+                if n == 0:
+                    continue
+                d = done[at]
+                tokens[i - a, :n] = torch.tensor(p[d:d + n], **i32)
+                new[i - a] = n
+                pages += self.slot_req[i]["pages"][-(-d // S):-(-(d + n) // S)]
+                done[at] = d + n
+            self.engine.prefill(view, tokens, new, torch.tensor(pages, **i32))
 
     # ---- slot moves -----------------------------------------------------------------------------
     def _swap(self, i: int, j: int) -> None:

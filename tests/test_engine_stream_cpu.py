@@ -57,7 +57,7 @@ def test_calls_are_ordered_with_the_current_stream(monkeypatch, fail, same):
     monkeypatch.setattr(torch.cuda, "stream", under)
     eng = FocusEngine(Context(log, current, fail), StepParams(), stream=own, chunk=object())
     i32 = dict(dtype=torch.int32)
-    view = {"block_tokens": torch.zeros(2, 8, **i32)}
+    view = {"block_tokens": torch.zeros(2, 8, **i32), "prefix_len": torch.zeros(2, **i32)}
     for what, call in (("step", lambda: eng.step(view, True)), ("commit", lambda: eng.commit(view)),
                        ("prefill", lambda: eng.prefill(view, torch.zeros(2, 3, **i32), torch.ones(2, **i32), torch.zeros(1, **i32)))):
         del log[:]
