@@ -7,8 +7,9 @@ every step and every commit runs through an engine (``FocusEngine``: the library
 ``focus_commit_block``); nothing of the method's arithmetic is here.
 
 Requests arrive with their prompt already in the KV pool (the step serves blocks on top of an exactly
-cached prefix, project page, Overview -- Motivation), or with its tokens, which are then run through the model
-in chunks at admission (``focus_prefill``), and ask for a number of blocks.  Each block of
+cached prefix, project page, Overview -- Motivation), or with its tokens, and ask for a number of blocks.  The
+tokens are run through the model in chunks (``focus_prefill``), one call per iteration for all requests that still
+have some, so that a long prompt does not hold up the requests that are running.  Each block of
 each request goes through the block loop of ``focus_decode_block``: a dense first step, focused steps
 until no position is masked, a dense refresh, and the commit of the block's K/V into the prefix pages.
 Requests sit in the slots of one batch; they are in different phases of that loop at the same time, so
@@ -45,7 +46,7 @@ from . import StepOutputs
 
 __all__ = ["Request", "RequestResult", "IterationStats", "EffectiveBatchScheduler", "FocusEngine"]
 
-_DENSE_FIRST, _FOCUSED, _DENSE_REFRESH = 0, 1, 2
+_DENSE_FIRST, _FOCUSED, _DENSE_REFRESH, _PROMPT = 0, 1, 2, 3
 
 
 @dataclasses.dataclass
@@ -78,6 +79,7 @@ class IterationStats:
     row_cost: int                 # focused * k_max + dense * B: rows run, at most row_budget
     committed: int                # blocks committed at the end of the iteration
     deferred: int = 0             # requests whose dense step waits for a later iteration (budget full)
+    prompts: int = 0              # requests whose prompt is not all cached yet
 
 
 class FocusEngine:
@@ -251,7 +253,6 @@ class EffectiveBatchScheduler:
         rec["block_steps"] = 0
 
     def _admit(self) -> None:
-        fresh: List[int] = []
         while self.waiting and self.waiting[0].arrival <= self.iteration and len(self.slot_req) < self.slots:
             req = self.waiting[0]
             cost = sum(self._cost(r) for r in self.slot_req)
@@ -270,33 +271,32 @@ class EffectiveBatchScheduler:
             self.slot_req.append(rec)
             self._write_slot(len(self.slot_req) - 1, rec)
             if req.prompt_tokens:
-                fresh.append(len(self.slot_req) - 1)
-        if fresh:
-            self._prefill(fresh)
+                rec["phase"], rec["cached"] = _PROMPT, 0
+                self.prefix_len[len(self.slot_req) - 1] = 0
 
-    def _prefill(self, slots: List[int]) -> None:
-        """Run the prompts of these slots through the model, several requests' chunks per call.  A chunk ends at the
+    def _prefill(self) -> None:
+        """Run a chunk of the prompts that are not all cached yet through the model, in one call.  A chunk ends at the
         prompt's end or at a multiple of the mask's block, whose positions see one another."""
-        rows, step, S = self.engine.prefill_rows(), self.engine.mask_block, self.page_size
-        i32 = dict(dtype=torch.int32)
-        a, b = slots[0], slots[-1] + 1
-        view = self._view(a, b)
-        prompts = [self.slot_req[i]["req"].prompt_tokens for i in slots]
-        for i in slots:
-            self.prefix_len[i] = 0
-        done = [0] * len(slots)
-        while any(len(p) > d for p, d in zip(prompts, done)):
-            take = share_rows([len(p) - d for p, d in zip(prompts, done)], rows, step)
-            tokens, new, pages = torch.zeros(b - a, max(take), **i32), torch.zeros(b - a, **i32), []
-            for at, (i, p, n) in enumerate(zip(slots, prompts, take)):
-                if n == 0:
-                    continue
-                d = done[at]
-                tokens[i - a, :n] = torch.tensor(p[d:d + n], **i32)
-                new[i - a] = n
-                pages += self.slot_req[i]["pages"][-(-d // S):-(-(d + n) // S)]
-                done[at] = d + n
-            self.engine.prefill(view, tokens, new, torch.tensor(pages, **i32))
+        slots = [i for i, rec in enumerate(self.slot_req) if rec["phase"] == _PROMPT]
+        if not slots:
+            return
+        step, S, i32 = getattr(self.engine, "mask_block", 1), self.page_size, dict(dtype=torch.int32)
+        recs = [self.slot_req[i] for i in slots]
+        take = share_rows([rec["req"].prompt_len - rec["cached"] for rec in recs], self.engine.prefill_rows(), step)
+        a, b = slots[0], slots[-1] + 1      # (the slots between them get no new tokens)
+        tokens, new, pages = torch.zeros(b - a, max(take), **i32), torch.zeros(b - a, **i32), []
+        for i, rec, n in zip(slots, recs, take):
+            if n == 0:
+                continue
+            d = rec["cached"]
+            tokens[i - a, :n] = torch.tensor(rec["req"].prompt_tokens[d:d + n], **i32)
+            new[i - a] = n
+            pages += rec["pages"][-(-d // S):-(-(d + n) // S)]
+        self.engine.prefill(self._view(a, b), tokens, new, torch.tensor(pages, **i32))
+        for rec, n in zip(recs, take):
+            rec["cached"] += n
+            if rec["cached"] == rec["req"].prompt_len:
+                rec["phase"] = _DENSE_FIRST
 
     # ---- slot moves -----------------------------------------------------------------------------
     def _swap(self, i: int, j: int) -> None:
@@ -321,9 +321,10 @@ class EffectiveBatchScheduler:
             self._swap(lo, hi)
 
     def _order_dense(self, start: int) -> None:
-        """Sort the dense slots [start, n) by admission (oldest first), so the ones that fit come first."""
+        """Sort the dense slots [start, n) by admission (oldest first), so the ones that fit come first; those whose
+        prompt is not all cached come last."""
         n = len(self.slot_req)
-        key = lambda i: (self.slot_req[i]["admitted"], self.slot_req[i]["req"].rid)
+        key = lambda i: (self.slot_req[i]["phase"] == _PROMPT, self.slot_req[i]["admitted"], self.slot_req[i]["req"].rid)
         for i in range(start, n):  # selection sort through slot swaps (a handful of slots)
             j = min(range(i, n), key=key)
             self._swap(i, j)
@@ -337,14 +338,16 @@ class EffectiveBatchScheduler:
         return not self.waiting and not self.slot_req
 
     def iterate(self) -> IterationStats:
-        """Admit, run the focused and the dense steps, move every request to its next phase, commit the
-        blocks whose refresh ran, retire finished requests."""
+        """Admit, run a chunk of the prompts, the focused and the dense steps, move every request to its next phase,
+        commit the blocks whose refresh ran, retire finished requests."""
         self._admit()
+        self._prefill()
         n_active = len(self.slot_req)
         n_f = self._partition()
         self._order_dense(n_f)
         fit = (self.row_budget - n_f * self.k_max) // self.B
-        n = n_f + max(0, min(n_active - n_f, fit))     # slots [0, n) run; dense slots beyond wait
+        prompts = sum(rec["phase"] == _PROMPT for rec in self.slot_req)
+        n = n_f + max(0, min(n_active - prompts - n_f, fit))   # slots [0, n) run; dense slots beyond wait
         cost = n_f * self.k_max + (n - n_f) * self.B
         if n_f > 0:
             self.engine.step(self._view(0, n_f), dense=False)
@@ -382,7 +385,8 @@ class EffectiveBatchScheduler:
             if not self.keep_pages:
                 self.free.extend(rec["pages"])
             self.free.extend(rec["reserved"])  # none left once every block is placed
-        st = IterationStats(self.iteration, n_active, n_f, n - n_f, cost, committed, n_active - n)
+        st = IterationStats(self.iteration, n_active, n_f, n - n_f, cost, committed, n_active - prompts - n,
+                            prompts)
         self.stats.append(st)
         self.iteration += 1
         return st

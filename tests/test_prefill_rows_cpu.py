@@ -4,7 +4,9 @@ import pytest
 import torch
 
 import focus_synth as fs
-from test_scheduler_cpu import B, S
+from prefill_reference import cached, prompt_forward
+from test_prefill_cpu import PromptEngine, _run
+from test_scheduler_cpu import B, MAX_PAGES, S
 from decodability_aware_token_b200 import StepParams
 from decodability_aware_token_b200.scheduler import EffectiveBatchScheduler, FocusEngine, Request, share_rows
 
@@ -57,3 +59,69 @@ def test_the_engine_runs_the_model_on_the_rows_that_hold_tokens():
         sch.submit(Request(r, 0, n, [], 1, prompt_tokens=list(range(n))))
     sch.run(max_iterations=50)
     assert [(rows, live) for rows, live, _ in seen] == [(745, 745)] and seen[0][2] == (16, 700)
+
+
+def test_a_long_prompt_does_not_hold_up_the_requests_that_run():
+    """One chunk of prompts per iteration: the running requests step in between, finish when they finish without the
+    long prompt, and everybody decodes what it decodes when its prompt was cached before."""
+    case = fs.make_case("tiny")
+    s, w = case.shape, case.work
+    g = torch.Generator().manual_seed(7)
+    short = {r: torch.randint(0, s.vocab, (n,), generator=g).tolist() for r, n in ((0, 5), (1, 3))}
+    prompts = {**short, 2: torch.randint(0, s.vocab, (40,), generator=g).tolist()}
+    kv = {r: prompt_forward(s, case.model, t, 1)[0] for r, t in prompts.items()}
+
+    def run(which):
+        pool = torch.zeros(40, s.n_layers, 2, s.n_kv_heads, S, s.head_dim, dtype=torch.float64)
+        eng = PromptEngine(case, which, kv, 8, 1)
+        calls = []
+        for what in ("prefill", "step"):
+            def note(*a, _f=getattr(eng, what), _w=what, **k):
+                calls.append(_w)
+                return _f(*a, **k)
+            setattr(eng, what, note)
+        sch = EffectiveBatchScheduler(eng, slots=3, block=B, n_layers=s.n_layers, n_kv_heads=s.n_kv_heads,
+                                      head_dim=s.head_dim, max_pages_per_req=MAX_PAGES, kv_pool=pool,
+                                      free_pages=list(range(40)), mask_token=s.vocab - 1, k_max=w.k_max, keep_pages=True)
+        for r, toks in which.items():
+            sch.submit(Request(r, 0 if r < 2 else 1, len(toks), [], 1, prompt_tokens=toks))
+        return sch.run(max_iterations=200), calls, sch
+    res, calls, sch = run(prompts)
+    alone, _, _ = run(short)
+    assert calls.count("prefill") == 6                                  # 8 tokens of the short ones, 40 of the long one
+    text = " ".join(calls)
+    assert "prefill prefill" not in text                                # running requests step between the chunks
+    assert [st.prompts for st in sch.stats[:7]] == [0, 1, 1, 1, 1, 0, 0] and all(st.deferred == 0 for st in sch.stats)
+    for r in short:
+        assert res[r].finished == alone[r].finished and [b.tolist() for b in res[r].blocks] == [b.tolist() for b in alone[r].blocks]
+    _, want, _ = _run(case, prompts, kv, False, 8, 1)
+    for r in prompts:
+        assert [b.tolist() for b in res[r].blocks] == [b.tolist() for b in want[r].blocks]
+        np.testing.assert_array_equal(cached(sch.kv_pool, res[r].pages, len(prompts[r])), kv[r])
+
+
+def test_prompts_that_are_not_cached_yet_wait_behind_the_others():
+    """More requests than the row budget runs at once, prompts among them: nothing steps on a prompt that is half done."""
+    case = fs.make_case("tiny")
+    s, w = case.shape, case.work
+    g = torch.Generator().manual_seed(11)
+    prompts = {r: torch.randint(0, s.vocab, (n,), generator=g).tolist() for r, n in enumerate((9, 33, 2, 40, 17, 26))}
+    kv = {r: prompt_forward(s, case.model, t, 1)[0] for r, t in prompts.items()}
+    pool = torch.zeros(60, s.n_layers, 2, s.n_kv_heads, S, s.head_dim, dtype=torch.float64)
+    eng = PromptEngine(case, prompts, kv, 11, 1)
+    sch = EffectiveBatchScheduler(eng, slots=5, block=B, n_layers=s.n_layers, n_kv_heads=s.n_kv_heads, head_dim=s.head_dim,
+                                  max_pages_per_req=MAX_PAGES, kv_pool=pool, free_pages=list(range(60)),
+                                  mask_token=s.vocab - 1, k_max=w.k_max, row_budget=3 * B, keep_pages=True)
+    step = eng.step
+
+    def checked(view, dense):
+        assert set(view["prefix_len"].tolist()) <= {len(t) + more for t in prompts.values() for more in (0, B)}
+        step(view, dense)
+    eng.step = checked
+    for r, toks in prompts.items():
+        sch.submit(Request(r, 0, len(toks), [], 2, prompt_tokens=toks))
+    res = sch.run(max_iterations=400)
+    _, want, _ = _run(case, prompts, kv, False, 11, 1)
+    for r in prompts:
+        assert res[r].blocks[0].tolist() == want[r].blocks[0].tolist()
+        np.testing.assert_array_equal(cached(pool, res[r].pages, len(prompts[r])), kv[r])
