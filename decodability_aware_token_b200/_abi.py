@@ -3,9 +3,11 @@ import ctypes as C
 import importlib.util
 import os
 import struct
+import sysconfig
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfocus.so")
 MARSHAL_PATH = os.path.join(os.path.dirname(LIB_PATH), "_marshal.so")
+MARSHAL_STAMP = os.path.join(os.path.dirname(LIB_PATH), "_marshal.abi")  # what _marshal.so was built for (build.py)
 
 FOCUS_OK = 0
 FOCUS_ERR_INVALID_ARG = -1
@@ -138,15 +140,33 @@ def load_enqueue():
     return _enqueue
 
 
+def marshal_abi():
+    """The interfaces _marshal.so is compiled against: torch, its C++ ABI, the Python ABI."""
+    import torch
+    return f"torch {torch.__version__}, cxx11 abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)}, {sysconfig.get_config_var('SOABI')}"
+
+
+def marshal_stamp():
+    """marshal_abi() at the time _marshal.so was built, None if it is not known."""
+    try:
+        with open(MARSHAL_STAMP) as f:
+            return f.read().strip()
+    except OSError:
+        return None
+
+
 def load_marshal():
     """The extension that reads the chunk operators' tensors in C++ (csrc/marshal.cpp) and the addresses of the three
-    entry points, for it to call.  ImportError if it was not built, or was built for another torch."""
+    entry points, for it to call.  ImportError if it was not built, or was built for another torch or Python."""
     global _marshal
     if _marshal is None:
         import torch  # (its libraries have to be loaded first)
         lib = load()
         if not os.path.exists(MARSHAL_PATH):
             raise ImportError(f"{MARSHAL_PATH} is missing: build it with `python -m decodability_aware_token_b200.build`")
+        if marshal_stamp() not in (None, marshal_abi()):  # (before it is loaded: it might not even link)
+            raise ImportError(f"{MARSHAL_PATH} was built for {marshal_stamp()}, this is {marshal_abi()}: rebuild it with "
+                              "`python -m decodability_aware_token_b200.build`")
         spec = importlib.util.spec_from_file_location(__package__ + "._marshal", MARSHAL_PATH)
         mod = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(mod)

@@ -4,7 +4,8 @@
 
 Each .cu under csrc/ compiles to an object under _build/ (in parallel, skipped when up to date),
 then everything links into decodability_aware_token_b200/libfocus.so.  csrc/marshal.cpp, the chunk operators'
-host binding, compiles with the host compiler against torch's headers into _marshal.so beside it.
+host binding, compiles with the host compiler against torch's headers into _marshal.so beside it; _marshal.abi names the
+torch and Python it was compiled for, so that another one rebuilds it.
 """
 from __future__ import annotations
 
@@ -17,12 +18,14 @@ import sys
 import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
+from . import _abi
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfocus.so")
-MARSHAL = os.path.join(PKG, "_marshal.so")
+MARSHAL, STAMP = _abi.MARSHAL_PATH, _abi.MARSHAL_STAMP
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -44,7 +47,8 @@ def _deps() -> list[str]:
 def build_marshal(force: bool = False) -> str:
     src = os.path.join(CSRC, "marshal.cpp")
     newest = max(os.path.getmtime(p) for p in (src, os.path.join(ROOT, "include", "focus.h")))
-    if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= newest:
+    abi = _abi.marshal_abi()
+    if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= newest and _abi.marshal_stamp() == abi:
         return MARSHAL
     import torch
     from torch.utils.cpp_extension import include_paths, library_paths
@@ -57,6 +61,8 @@ def build_marshal(force: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed on {src}:\n{r.stdout}\n{r.stderr}")
+    with open(STAMP, "w") as f:
+        f.write(abi + "\n")
     return MARSHAL
 
 
