@@ -43,7 +43,7 @@ struct ChunkAttnDev {
     // the other one: its CTAs start as the SMs come free, and it only waits at its end, so that who waits for it
     // has waited for both (40 single tokens and 8 chunks: 308 -> 292 us).
     bool pair;
-    bool small_walk;  // the launch's key blocks, and their products with the CTA count, fit 31 bits
+    bool small_walk;  // the launch's key blocks fit 31 bits, as long as the requests' row ranges do not overlap
     // scratch of units whose key walk is split over CTAs: slot 2c / 2c + 1 is CTA c's first / last piece
     float* part_o;
     float* part_ml;

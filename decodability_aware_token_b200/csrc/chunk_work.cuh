@@ -20,13 +20,14 @@ struct ChunkReq {
 };
 
 // Request b's rows and keys; a request whose numbers are out of range is flagged and skipped.  (Read from L2: a kernel
-// that does not wait for the one before it must not meet an old line.)
-__device__ __forceinline__ ChunkReq chunk_req(const ChunkAttnDev& a, int b, bool flag) {
+// that does not wait for the one before it must not meet an old line.)  *back becomes 1 where the row offsets decrease.
+__device__ __forceinline__ ChunkReq chunk_req(const ChunkAttnDev& a, int b, bool flag, int* back = nullptr) {
     ChunkReq r;
     r.row0 = __ldcg(a.row_offsets + b);
     const int end = __ldcg(a.row_offsets + b + 1);
     r.kv = __ldcg(a.kv_len + b);
     r.n = 0;
+    if (back != nullptr && end < r.row0) *back = 1;
     if (r.row0 < 0 || end < r.row0 || end > a.rows || end - r.row0 > a.max_new) {
         if (flag) raise_err(a.err, FOCUS_DEVERR_ROWS);
     } else if (r.kv < 0 || r.kv > a.max_pages * a.S) {
@@ -109,12 +110,13 @@ __device__ void chunk_schedule(const ChunkAttnDev& a, const ChunkShape& sh, long
     int any_long = 0;
     if (a.N <= nt && a.small_walk) {
         // a request per thread, sums in registers and 32 bits, three barriers; falls through if some request has
-        // many tiles
+        // many tiles, or if the row offsets decrease somewhere: the ranges behind and before that place may overlap, and
+        // the sums be many times what a.small_walk allows for
         ChunkReq r{};
         int tiles = 0;
         uint32_t s = 0;
         if (tid < a.N) {
-            r = chunk_req(a, tid, blockIdx.x == 0);
+            r = chunk_req(a, tid, blockIdx.x == 0, &any_long);
             tiles = chunk_tiles(a, sh, r);
             if (tiles > kSerial) any_long = 1;
             else
