@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes as C
 import dataclasses
+import math
 from typing import Optional
 
 import torch
@@ -236,8 +237,9 @@ class ChunkContext:
         (focus_chunk_attention).  `max_new` bounds the rows of a request (default: all rows); a tight bound
         saves work.  mask_block 1 is the causal mask, B the block-causal mask of blocks of B positions."""
         where = "focus_chunk_attention"
-        if (self._marshal and out is not None and max_new is not None and _current_device() == self._index and
-                (scale is None or scale > 0)):
+        if scale is not None and not 0 < C.c_float(scale).value < math.inf:  # (0 would stand for 1 / sqrt(d))
+            raise ValueError(f"scale {scale}: must be positive and finite in float32")
+        if self._marshal and out is not None and max_new is not None and _current_device() == self._index:
             rc = self._marshal.attention(
                 self._entry[2], self._ctx.value, self._stream(stream, where), self._index, self._elt == 2, self.n_q_heads,
                 self.n_kv_heads, self.head_dim, self.cfg.n_layers, self.limits.max_pages_per_req, layer, max_new, mask_block,
@@ -255,13 +257,10 @@ class ChunkContext:
         n_pages, page_size, pool = self._pool(kv_pool, layer)
         if max_new is None:
             max_new = max(rows, 1)
-        if scale is None:
-            scale = 0.0
-        elif not scale > 0:
-            raise ValueError(f"scale {scale}: must be positive")
-        args = _abi.ATTN_PACK.pack(n, rows, max_new, page_size, n_pages, layer, mask_block, scale, qs, os_, qp, pool,
-                                   self._ints(row_offsets, "row_offsets", (n + 1,)), self._ints(kv_len, "kv_len", (n,)),
-                                   self._ints(page_table, "page_table", (n, self.limits.max_pages_per_req)), op)
+        i, row = self._ints, (n, self.limits.max_pages_per_req)
+        args = _abi.ATTN_PACK.pack(n, rows, max_new, page_size, n_pages, layer, mask_block, 0.0 if scale is None else scale,
+                                   qs, os_, qp, pool, i(row_offsets, "row_offsets", (n + 1,)), i(kv_len, "kv_len", (n,)),
+                                   i(page_table, "page_table", row), op)
         self._call(2, args, where, stream)
         return out
 
