@@ -305,8 +305,8 @@ class FocusContext:
 
     def close(self):
         if getattr(self, "_ctx", None) is not None and self._ctx.value:
-            _check(self._lib.focus_destroy(self._ctx), "focus_destroy")
-            self._ctx = C.c_void_p()
+            ctx, self._ctx = self._ctx, C.c_void_p()  # (freed whatever the status is)
+            _check(self._lib.focus_destroy(ctx), "focus_destroy")
 
     def __enter__(self):
         return self

@@ -22,3 +22,23 @@ def test_a_scale_that_float32_cannot_hold_is_refused():
     for scale in (1.5e-45, 1e-38, 0.25, 3e38):
         ctx.attention(**a, scale=scale)
         assert _abi.ChunkAttnArgs.from_buffer_copy(calls[-1][1]).scale == C.c_float(scale).value > 0
+
+
+@pytest.mark.parametrize("cls,fn", [(ChunkContext, "focus_chunk_destroy"), (FocusContext, "focus_destroy")])
+@pytest.mark.parametrize("rc", [_abi.FOCUS_OK, _abi.FOCUS_ERR_CUDA])
+def test_a_context_is_destroyed_once_whatever_the_status(cls, fn, rc):
+    """The library frees the context also when it reports an error: nothing may be handed to it again."""
+    seen = []
+
+    class Lib:
+        pass
+    setattr(Lib, fn, lambda self, ctx: (seen.append(ctx.value), rc)[1])
+    ctx = cls.__new__(cls)
+    ctx._ctx, ctx._lib = C.c_void_p(0x1000), Lib()
+    if rc:
+        with pytest.raises(FocusError):
+            ctx.close()
+    ctx.close()
+    ctx.close()
+    del ctx
+    assert seen == [0x1000]
