@@ -120,6 +120,9 @@ class FocusEngine:
             raise ValueError(f"{slots} slots exceed the context's max_requests ({lim.max_requests})")
         if block > lim.max_block or block > lim.max_keep:
             raise ValueError(f"block {block}: the context needs max_block and max_keep >= B for the dense steps")
+        if self.chunk is not None and self.chunk.limits.max_pages_per_req != lim.max_pages_per_req:
+            raise ValueError(f"chunk: page tables of {self.chunk.limits.max_pages_per_req} entries, the context's have "
+                             f"{lim.max_pages_per_req}")
 
     def _outputs(self, n: int, block: int):
         if self._out is None or self._out.keep_count.shape[0] < n or self._out.decoded_ids.shape[1] != block:
@@ -140,6 +143,10 @@ class FocusEngine:
     def prefill_rows(self) -> int:
         """Prompt tokens one call takes (0: no prompts)."""
         return 0 if self.chunk is None else self.ctx.limits.max_requests * self.ctx.limits.max_block
+
+    def prefill_requests(self) -> int:
+        """Slots one call takes."""
+        return self.chunk.limits.max_requests
 
     def prefill(self, view: Dict[str, torch.Tensor], tokens: torch.Tensor, new_len: torch.Tensor,
                 pages: torch.Tensor) -> None:
@@ -280,6 +287,8 @@ class EffectiveBatchScheduler:
         slots = [i for i, rec in enumerate(self.slot_req) if rec["phase"] == _PROMPT]
         if not slots:
             return
+        most = getattr(self.engine, "prefill_requests", lambda: self.slots)()
+        slots = [i for i in slots if i < slots[0] + most]
         step, S, i32 = getattr(self.engine, "mask_block", 1), self.page_size, dict(dtype=torch.int32)
         recs = [self.slot_req[i] for i in slots]
         take = share_rows([rec["req"].prompt_len - rec["cached"] for rec in recs], self.engine.prefill_rows(), step)

@@ -1,4 +1,6 @@
 """Prompts in the scheduler, on the CPU: how a call's rows are shared among them, and on how many rows the model runs."""
+from types import SimpleNamespace
+
 import numpy as np
 import pytest
 import torch
@@ -48,7 +50,7 @@ def test_the_engine_runs_the_model_on_the_rows_that_hold_tokens():
             seen.append((rows, int(new_len.sum()), tuple(tokens.shape)))
             batch["prefix_len"] += new_len
     s = fs.make_case("tiny").shape
-    eng = FocusEngine(Context(), StepParams(), chunk=object())
+    eng = FocusEngine(Context(), StepParams(), chunk=SimpleNamespace(limits=SimpleNamespace(max_requests=16)))
     eng.step = lambda view, dense: view["mask"].zero_()
     eng.commit, eng.capacity_check = (lambda view: None), (lambda slots, block: None)
     sch = EffectiveBatchScheduler(eng, slots=16, block=B, n_layers=s.n_layers, n_kv_heads=s.n_kv_heads, head_dim=s.head_dim,
@@ -125,3 +127,40 @@ def test_prompts_that_are_not_cached_yet_wait_behind_the_others():
     for r in prompts:
         assert res[r].blocks[0].tolist() == want[r].blocks[0].tolist()
         np.testing.assert_array_equal(cached(pool, res[r].pages, len(prompts[r])), kv[r])
+
+
+@pytest.mark.parametrize("most", [1, 2])
+def test_calls_span_no_more_slots_than_the_chunk_context_takes(most):
+    case = fs.make_case("tiny")
+    s, w = case.shape, case.work
+    g = torch.Generator().manual_seed(5)
+    prompts = {r: torch.randint(0, s.vocab, (n,), generator=g).tolist() for r, n in enumerate((9, 21, 0, 14, 30))}
+    none = np.zeros((s.n_layers, 2, s.n_kv_heads, 0, s.head_dim))
+    kv = {r: prompt_forward(s, case.model, t, 1)[0] if t else none for r, t in prompts.items()}
+    eng = PromptEngine(case, prompts, kv, 16, 1)
+    eng.prefill_requests = lambda: most
+    prefill = eng.prefill
+
+    def checked(view, tokens, new_len, pages):
+        assert 1 <= len(new_len) == tokens.shape[0] == view["prefix_len"].shape[0] <= most
+        prefill(view, tokens, new_len, pages)
+    eng.prefill = checked
+    pool = torch.zeros(60, s.n_layers, 2, s.n_kv_heads, S, s.head_dim, dtype=torch.float64)
+    sch = EffectiveBatchScheduler(eng, slots=5, block=B, n_layers=s.n_layers, n_kv_heads=s.n_kv_heads, head_dim=s.head_dim,
+                                  max_pages_per_req=MAX_PAGES, kv_pool=pool, free_pages=list(range(60)),
+                                  mask_token=s.vocab - 1, k_max=w.k_max, keep_pages=True)
+    for r, toks in prompts.items():
+        sch.submit(Request(r, 0, len(toks), [], 1, prompt_tokens=toks))
+    res = sch.run(max_iterations=300)
+    for r in prompts:
+        np.testing.assert_array_equal(cached(pool, res[r].pages, len(prompts[r])), kv[r])
+
+
+def test_the_engine_refuses_a_chunk_context_with_other_page_tables():
+    NS = SimpleNamespace
+    ctx = NS(limits=NS(max_requests=4, max_block=64, max_keep=64, max_pages_per_req=9))
+    eng = lambda pages, n=4: FocusEngine(ctx, StepParams(), chunk=NS(limits=NS(max_requests=n, max_pages_per_req=pages)))
+    eng(9).capacity_check(4, 16)
+    assert eng(9, 3).prefill_requests() == 3
+    with pytest.raises(ValueError):
+        eng(8).capacity_check(4, 16)
