@@ -69,6 +69,29 @@ bool rows_ok(const focus_chunk_ctx* c, const void* p, int64_t stride, int heads)
            stride < ((int64_t)1 << 40);
 }
 
+// The bytes of `rows` rows of `heads` heads, `stride` elements apart.
+struct Span {
+    uintptr_t at, end, step, len;
+};
+Span span_of(const focus_chunk_ctx* c, const void* p, int64_t stride, int heads, int rows) {
+    const uintptr_t e = elt_of(c), at = reinterpret_cast<uintptr_t>(p), len = (uintptr_t)heads * c->cfg.head_dim * e,
+                    step = (uintptr_t)stride * e;
+    return {at, at + (uintptr_t)(rows - 1) * step + len, step, len};
+}
+// Do two sets of rows share a byte?  Views of one buffer have the same step, and their rows lie side by side or do not;
+// rows that interleave at different steps count as sharing.
+bool share(const Span& x, const Span& y) {
+    if (x.end <= y.at || y.end <= x.at) return false;
+    if (x.step != y.step) return true;
+    const uintptr_t d = y.at >= x.at ? (y.at - x.at) % x.step : (x.step - (x.at - y.at) % x.step) % x.step;
+    return d < x.len || d + y.len > x.step;
+}
+bool in_pool(const focus_chunk_ctx* c, const Span& x, const void* pool, int64_t n_pages, int64_t page_size) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(pool), bytes = (uintptr_t)n_pages * (uintptr_t)c->cfg.n_layers * 2 *
+                                                                   c->cfg.n_kv_heads * (uintptr_t)page_size * c->cfg.head_dim * elt_of(c);
+    return x.at < at + bytes && at < x.end;
+}
+
 struct Range {
     explicit Range(const char* n) { nvtxRangePushA(n); }
     ~Range() { nvtxRangePop(); }
@@ -191,7 +214,13 @@ int focus_chunk_qk_norm_rope(focus_chunk_ctx* c, const focus_chunk_qk* p, void* 
     if (p->rows == 0) return FOCUS_OK;
     const int hq = c->cfg.n_q_heads, hkv = c->cfg.n_kv_heads;
     if (!rows_ok(c, p->q, p->q_stride, hq) || !rows_ok(c, p->k, p->k_stride, hkv) || !rows_ok(c, p->v, p->v_stride, hkv) ||
-        !rows_ok(c, p->q_out, p->out_stride, hq) || (p->q_out == p->q && p->out_stride != p->q_stride))
+        !rows_ok(c, p->q_out, p->out_stride, hq))
+        return FOCUS_ERR_INVALID_ARG;
+    const Span out = span_of(c, p->q_out, p->out_stride, hq, p->rows);
+    const bool in_place = p->q_out == p->q && p->out_stride == p->q_stride;
+    if ((!in_place && share(out, span_of(c, p->q, p->q_stride, hq, p->rows))) ||
+        share(out, span_of(c, p->k, p->k_stride, hkv, p->rows)) || share(out, span_of(c, p->v, p->v_stride, hkv, p->rows)) ||
+        in_pool(c, out, p->kv_pool, p->n_pages, p->page_size))
         return FOCUS_ERR_INVALID_ARG;
     if (!p->row_pos || !p->row_slot || !aligned(p->row_pos, 4) || !aligned(p->row_slot, 4) ||
         (p->n_pages > 0 && !p->kv_pool) || !aligned(p->kv_pool, 16) || !aligned(p->q_norm, 16) || !aligned(p->k_norm, 16))
@@ -221,9 +250,12 @@ int focus_chunk_attention(focus_chunk_ctx* c, const focus_chunk_attn* p, void* s
     if (bf && p->page_size != 16 && p->page_size != 32 && p->page_size != 64) return FOCUS_ERR_UNSUPPORTED;
     if (p->n_requests == 0 || p->rows == 0) return FOCUS_OK;
     const int hq = c->cfg.n_q_heads, hkv = c->cfg.n_kv_heads;
-    if (!rows_ok(c, p->q, p->q_stride, hq) || !rows_ok(c, p->out, p->out_stride, hq) || p->out == p->q ||
+    if (!rows_ok(c, p->q, p->q_stride, hq) || !rows_ok(c, p->out, p->out_stride, hq) ||
         !p->row_offsets || !p->kv_len || !p->page_table || !aligned(p->row_offsets, 4) || !aligned(p->kv_len, 4) ||
         !aligned(p->page_table, 4) || (p->n_pages > 0 && !p->kv_pool) || !aligned(p->kv_pool, 16))
+        return FOCUS_ERR_INVALID_ARG;
+    const Span out = span_of(c, p->out, p->out_stride, hq, p->rows);
+    if (share(out, span_of(c, p->q, p->q_stride, hq, p->rows)) || in_pool(c, out, p->kv_pool, p->n_pages, p->page_size))
         return FOCUS_ERR_INVALID_ARG;
     if (!device_ok(c)) return FOCUS_ERR_INVALID_ARG;
     ChunkAttnDev a{};

@@ -393,7 +393,8 @@ int focus_chunk_plan_rows(focus_chunk_ctx* ctx, const focus_chunk_plan* p, void*
  * queries go to q_out, keys and (unchanged) values into the pool at row_slot, layer `layer`.
  * A row with row_pos < 0 is skipped (its q_out row stays as it was); a row with row_slot < 0 gets its
  * queries but is not stored; row_slot >= n_pages * S sets FOCUS_DEVERR_PAGE_ID and is not stored.  Slots of
- * stored rows must differ.  q_out may be q (same stride). */
+ * stored rows must differ.  q_out may be q (same pointer and stride); else it must not overlap q, and never k, v or the
+ * pool (FOCUS_ERR_INVALID_ARG). */
 typedef struct {
     int32_t rows;
     int32_t layer;
@@ -448,7 +449,7 @@ typedef struct {
     const int32_t* row_offsets;   /* [N + 1] */
     const int32_t* kv_len;        /* [N] */
     const int32_t* page_table;    /* [N, max_pages_per_req] */
-    void* out;                    /* [rows, Hq, d] T; must not overlap q */
+    void* out;                    /* [rows, Hq, d] T; must not overlap q or the pool (FOCUS_ERR_INVALID_ARG) */
 } focus_chunk_attn;
 /* Returns FOCUS_OK, FOCUS_ERR_INVALID_ARG, FOCUS_ERR_LIMITS (N, max_pages_per_req * S > 2^30, or a pool of
  * 2^31 key and value rows or more), FOCUS_ERR_UNSUPPORTED (bf16 page size) or FOCUS_ERR_CUDA. */

@@ -65,3 +65,52 @@ def test_attention_of_large_values_under_a_reference_that_lags(reqs, hq, hkv, la
         torch.cuda.synchronize()
         assert ctx.device_error() == (0, 0) and bool(torch.isfinite(out.float()).all())
         b.check(out)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("native", [True, False])
+def test_outputs_that_overlap_the_inputs_are_refused(dt, native):
+    from decodability_aware_token_b200 import FocusError
+    hq, hkv, d, T = 4, 2, 128, 6
+    b = Batch([(T, 20)], hq, hkv, d, dt, 16, seed=1)
+    pos, slot = torch.arange(T, dtype=torch.int32, device="cuda"), torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    wide = torch.randn(T + 2, 3 * hq + 2 * hkv, d, device="cuda").to(dt)          # q | k | v | two outputs' worth
+    q, k, v, rest = wide[:T, :hq], wide[:T, hq:hq + hkv], wide[:T, hq + hkv:hq + 2 * hkv], hq + 2 * hkv
+    flat = lambda t, at, n: t.flatten()[at:at + n * hq * d].view(n, hq, d)
+    whole = lambda n: wide.as_strided((n, hq, d), (hq * d, d, 1))                   # dense rows over the same memory
+    bad_qk = {"a head on": wide[:T, 1:hq + 1], "a row on": wide[1:T + 1, :hq], "into k": wide[:T, hq:2 * hq],
+              "into v": wide[:T, hq + 1:2 * hq + 1], "a row on, into v": wide[1:T + 1, hq + hkv:2 * hq + hkv],
+              "other stride": whole(T), "the pool": flat(b.pool, 0, T), "the pool's end": b.pool.flatten()[-T * hq * d:].view(T, hq, d)}
+    good_qk = {"in place": q, "beside": wide[:T, rest:rest + hq], "beside, two rows on": wide[2:, rest + hq:], "apart": torch.zeros(T, hq, d, dtype=dt, device="cuda")}
+    with _ctx(hq, hkv, d, dt, n=1, pages=b.max_pages) as ctx:
+        if not native:
+            ctx._marshal = None
+        keep = wide.clone(), b.pool.nan_to_num(nan=3.0).clone()
+        for what, out in bad_qk.items():
+            with pytest.raises(FocusError) as e:
+                ctx.qk_norm_rope(q, k, v, b.pool, 0, pos, slot, out=out)
+            assert e.value.code == -1, what
+            if what in ("into k", "into v", "a row on, into v"):
+                continue
+            with pytest.raises(FocusError) as e:
+                ctx.attention(q, b.pool, 1, b.row_offsets, b.kv_len, b.table, max_new=T, out=out)
+            assert e.value.code == -1, what
+        with pytest.raises(FocusError):                                               # attention is not done in place
+            ctx.attention(q, b.pool, 1, b.row_offsets, b.kv_len, b.table, max_new=T, out=q)
+        torch.cuda.synchronize()
+        assert torch.equal(wide, keep[0]) and torch.equal(b.pool.nan_to_num(nan=3.0), keep[1])
+        want = ctx.qk_norm_rope(q, k, v, b.pool, 0, pos, slot)
+        o = ctx.attention(q, b.pool, 1, b.row_offsets, b.kv_len, b.table)
+        for what, out in good_qk.items():
+            wide.copy_(keep[0])
+            if what != "in place":
+                assert torch.equal(ctx.attention(q, b.pool, 1, b.row_offsets, b.kv_len, b.table, max_new=T, out=out), o), what
+            assert torch.equal(ctx.qk_norm_rope(q, k, v, b.pool, 0, pos, slot, out=out), want), what
+            assert torch.equal(k, keep[0][:T, hq:hq + hkv]) and torch.equal(v, keep[0][:T, hq + hkv:hq + 2 * hkv])
+        # a single row has no stride
+        one = wide[:1, :hq]
+        with pytest.raises(FocusError):
+            ctx.qk_norm_rope(one, k[:1], v[:1], b.pool, 0, pos[:1], slot[:1], out=wide[:1, 2:hq + 2])
+        ctx.qk_norm_rope(one, k[:1], v[:1], b.pool, 0, pos[:1], slot[:1], out=wide[:1, rest:rest + hq])
+        torch.cuda.synchronize()
+        assert ctx.device_error() == (0, 0)
