@@ -9,8 +9,9 @@
 // 16 bytes of a head's lower half and the 16 bytes of the same pairs in its upper half, so the rotation needs
 // no exchange and every access is a full 16 bytes; D / 2 / (16 bytes) lanes form a head and a warp works
 // on several heads of one row at once.  A row's angles are computed once per warp and used for all its heads:
-// pos / pi theta^(-2i/d) in double, reduced to [-1, 1] exactly, then sincospif.  (Float angles lose
-// pos 2^-24 radians: 4e-3 at position 65536.)  The result is rounded once, to T.
+// pos / pi theta^(-2i/d) in double, less the nearest quarter turn, which leaves [-1/4, 1/4] exactly, then rounded to
+// float32 (off by at most 2^-27 half turns, 2.4e-8 radians; four times that if whole turns alone were taken off) for
+// sincospif.  (Float angles lose pos 2^-24 radians: 4e-3 at position 65536.)  The result is rounded once, to T.
 #include "chunk.h"
 
 namespace focus {
@@ -98,10 +99,12 @@ __global__ void __launch_bounds__(kThreads, 12) chunk_qk_kernel(ChunkQkDev a, in
 #pragma unroll
     for (int i = lane; i < D / 2; i += 32) {
         const double t = (double)pos * a.freq_over_pi[i];
+        const long long turn = __double2ll_rn(2.0 * t);  // quarter turns
         float s, c;
-        sincospif((float)(t - 2.0 * rint(0.5 * t)), &s, &c);
-        cos_s[warp][i] = c;
-        sin_s[warp][i] = s;
+        sincospif((float)(t - 0.5 * (double)turn), &s, &c);
+        const float x = turn & 1 ? s : c, y = turn & 1 ? c : s;  // a quarter turn: (c, s) -> (-s, c)
+        cos_s[warp][i] = (turn + 1) & 2 ? -x : x;
+        sin_s[warp][i] = turn & 2 ? -y : y;
     }
     __syncwarp();
     T* out = reinterpret_cast<T*>(p.q_out) + (long long)row * p.out_stride + c0;
