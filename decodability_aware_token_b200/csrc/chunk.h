@@ -16,10 +16,11 @@ struct ChunkPlanDev {
 };
 int launch_chunk_plan(const ChunkPlanDev& a, cudaStream_t s);
 bool configure_chunk_plan_kernel();
-// out[r] = the token of row r (0 for rows of nobody); then prefix_len[b] = kv_len[b]
-int launch_chunk_tokens(const focus_chunk_plan& p, const int32_t* tokens, int max_new, int32_t* out, int* err,
+// out[r] = the token of row r, at[r] its position (0 for rows of nobody); then prefix_len[b] = kv_len[b]
+int launch_chunk_tokens(const focus_chunk_plan& p, const int32_t* tokens, int max_new, int32_t* out, int32_t* at, int* err,
                         cudaStream_t s);
 const focus_chunk_cfg* chunk_cfg(const focus_chunk_ctx* c);
+int64_t chunk_positions(const focus_chunk_ctx* c, int page_size);  // positions a page table row reaches
 
 struct ChunkQkDev {
     focus_chunk_qk p;

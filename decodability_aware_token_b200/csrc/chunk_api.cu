@@ -23,6 +23,7 @@ struct focus_chunk_ctx {
 };
 
 const focus_chunk_cfg* focus::chunk_cfg(const focus_chunk_ctx* c) { return &c->cfg; }
+int64_t focus::chunk_positions(const focus_chunk_ctx* c, int page_size) { return (int64_t)c->lim.max_pages_per_req * page_size; }
 
 namespace {
 

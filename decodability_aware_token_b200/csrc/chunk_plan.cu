@@ -200,7 +200,8 @@ __global__ void __launch_bounds__(kThreads) chunk_plan_kernel(ChunkPlanDev a) {
 }
 
 __global__ void __launch_bounds__(kThreads) chunk_tokens_kernel(focus_chunk_plan p, const int32_t* __restrict__ tokens,
-                                                                int max_new, int32_t* __restrict__ out, int* err) {
+                                                                int max_new, int32_t* __restrict__ out,
+                                                                int32_t* __restrict__ row_at, int* err) {
     pdl_entry();
     const int i = blockIdx.x * kThreads + threadIdx.x;
     if (i < p.max_rows) {
@@ -212,17 +213,18 @@ __global__ void __launch_bounds__(kThreads) chunk_tokens_kernel(focus_chunk_plan
             else raise_err(err, FOCUS_DEVERR_ROWS);
         }
         out[i] = tok;
+        row_at[i] = max(p.row_pos[i], 0);
     }
     if (i < p.n_requests) const_cast<int32_t*>(p.prefix_len)[i] = p.kv_len[i];
 }
 
 }  // namespace
 
-int launch_chunk_tokens(const focus_chunk_plan& p, const int32_t* tokens, int max_new, int32_t* out, int* err,
+int launch_chunk_tokens(const focus_chunk_plan& p, const int32_t* tokens, int max_new, int32_t* out, int32_t* at, int* err,
                         cudaStream_t s) {
     const int n = p.max_rows > p.n_requests ? p.max_rows : p.n_requests;
     return launched(launch_pdl(chunk_tokens_kernel, dim3((n + kThreads - 1) / kThreads), dim3(kThreads), 0, s, 0, p, tokens,
-                               max_new, out, err));
+                               max_new, out, at, err));
 }
 
 bool configure_chunk_plan_kernel() {

@@ -42,7 +42,8 @@ struct focus_ctx {
     double* inv_freq;
     float2* rope_tab;     // bf16 path: [rope_positions][head_dim / 2] (cos, sin)
     int32_t* masked_count;  // block loop: masked positions left after a step
-    int32_t* zeros;         // [max_requests * max_block] zeros: prefix lengths of rows that are not rotated (prefill)
+    int32_t* zeros;         // [max_requests * max_block] zeros: positions of rows that are not rotated (prefill)
+    int32_t* row_at;        // [max_requests * max_block] positions of a chunk's rows (prefill)
     int32_t* req_order;     // [max_requests] requests by descending prefix length (kept-row attention order)
     int* err;
     float *att_part_o, *att_part_ml, *att_sb;
@@ -143,11 +144,11 @@ Layout plan(const focus_model_cfg* c, const focus_limits* l) {
         split * rope_positions(l) * (size_t)c->head_dim / 2 * 8,  // 23 RoPE (cos, sin) table
         64,                                                 // 24 block loop: masked-position count
         (size_t)l->max_requests * 4,                        // 25 request order
-        rows_full * 4,                                      // 26 zeros
+        rows_full * 4, rows_full * 4,                       // 26-27 zeros, row positions
     };
     Layout lay{};
     size_t at = 0;
-    for (int i = 0; i < 27; ++i) {
+    for (int i = 0; i < 28; ++i) {
         lay.off[i] = at;
         at = align_up(at + sizes[i], 1024);
     }
@@ -367,9 +368,12 @@ int run_step(focus_ctx* c, const focus_batch* in, const focus_params* p, focus_s
 }
 
 // A chunk of prompt tokens through the model (focus_prefill): the chunk operators between the step's own GEMMs and
-// row kernels.  The QKV projection's rows have to arrive unrotated: the tensor-core epilogue is given position 0 of
-// every row (a turn by 0, exact) and rows as blocks of one position, so that it leaves the queries in c->q and
-// keys and values side by side in c->part; the CUDA-core GEMM leaves the float32 row there as a whole.
+// row kernels.  Rows go through the tensor-core QKV epilogue as blocks of one position, which leaves the queries in c->q
+// and keys and values side by side in c->part.  Without head norms the epilogue rotates at each row's position, from float32
+// with one rounding as in the step, and the operator's rotation is a turn by 0 (exact).  Head norms come before the
+// rotation: then the epilogue turns by 0, which rounds the projection once more, and the operator norms and rotates; so
+// it does where the page table reaches beyond the epilogue's table of angles.  The CUDA-core GEMM leaves the
+// float32 row in c->part as a whole.
 template <typename T>
 int run_prefill(focus_ctx* c, focus_chunk_ctx* k, const focus_prefill_args* p, cudaStream_t s) {
     const Dims& dm = c->dm;
@@ -382,14 +386,15 @@ int run_prefill(focus_ctx* c, focus_chunk_ctx* k, const focus_prefill_args* p, c
     int rc = focus_chunk_plan_rows(k, &pl, s);
     if (rc != FOCUS_OK || T_rows == 0) return rc;
     int32_t* tok = reinterpret_cast<int32_t*>(c->act);  // read before the first MLP writes there
-    bool bad = launch_chunk_tokens(pl, p->tokens, p->max_new, tok, c->err, s) < 0;
+    const bool turned = tc && !p->q_norm && !p->k_norm && chunk_positions(k, pl.page_size) <= (int64_t)rope_positions(&c->lim);
+    bool bad = launch_chunk_tokens(pl, p->tokens, p->max_new, tok, c->row_at, c->err, s) < 0;
     bad = launch_embed_norm<T>(tok, T_rows, dm.V, W(c->embed), W(c->attn_norm[0]), dm.eps, dm.D, c->x_full, h, c->err, s) < 0 || bad;
     auto gemm = [&](Epi epi, const void* A, const void* Bw, const void* B2, int Nn, int K, float* resid) {
         GemmArgs g{};
         g.A = A; g.B = Bw; g.B2 = B2; g.M_bound = T_rows; g.N = Nn; g.K = K; g.splits = 1;
         g.part = c->part; g.split_stride = stride; g.act = c->act; g.resid = resid;
-        g.q_out = c->q; g.ibc = c->part; g.prefix_len = c->zeros; g.inv_freq = c->inv_freq; g.rope_tab = c->rope_tab;
-        g.max_prefix = 0; g.block = 1; g.n_layers = 1; g.layer = 0; g.Hq = dm.Hq; g.Hkv = dm.Hkv; g.err = c->err;
+        g.q_out = c->q; g.ibc = c->part; g.prefix_len = turned ? c->row_at : c->zeros; g.inv_freq = c->inv_freq;
+        g.rope_tab = c->rope_tab; g.max_prefix = turned ? (int)rope_positions(&c->lim) - 1 : 0; g.block = 1; g.n_layers = 1; g.layer = 0; g.Hq = dm.Hq; g.Hkv = dm.Hkv; g.err = c->err;
         if (tc) return tc_gemm(c->tc, epi, g, s);
         g.n_tiles = (Nn + kSimtTileN - 1) / kSimtTileN;
         g.tile_n = kSimtTileN;
@@ -397,7 +402,7 @@ int run_prefill(focus_ctx* c, focus_chunk_ctx* k, const focus_prefill_args* p, c
     };
     focus_chunk_qk qa{};
     qa.rows = T_rows; qa.page_size = pl.page_size; qa.n_pages = pl.n_pages; qa.eps = dm.eps;
-    qa.row_pos = pl.row_pos; qa.row_slot = pl.row_slot; qa.q_out = c->q; qa.out_stride = (int64_t)hd; qa.kv_pool = p->kv_pool;
+    qa.row_pos = turned ? c->zeros : pl.row_pos; qa.row_slot = pl.row_slot; qa.q_out = c->q; qa.out_stride = (int64_t)hd; qa.kv_pool = p->kv_pool;
     T* part = reinterpret_cast<T*>(c->part);
     qa.q = tc ? c->q : c->part;
     qa.q_stride = (int64_t)(tc ? hd : dm.qkv);
@@ -526,6 +531,7 @@ int focus_init(const focus_model_cfg* cfg, const focus_weights* w, const focus_l
     c->masked_count = reinterpret_cast<int32_t*>(base + lay.off[24]);
     c->req_order = reinterpret_cast<int32_t*>(base + lay.off[25]);
     c->zeros = reinterpret_cast<int32_t*>(base + lay.off[26]);
+    c->row_at = reinterpret_cast<int32_t*>(base + lay.off[27]);
     c->err = reinterpret_cast<int*>(base + lay.off[16]);
     c->att_part_o = reinterpret_cast<float*>(base + lay.off[17]);
     c->att_part_ml = reinterpret_cast<float*>(base + lay.off[18]);

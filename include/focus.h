@@ -457,8 +457,10 @@ int focus_chunk_attention(focus_chunk_ctx* ctx, const focus_chunk_attn* p, void*
 
 /* A chunk of prompt tokens through the whole model: plan, then per layer the QKV projection, norm + rotation +
  * cache write and the chunk's attention, O, SwiGLU; the prompt's keys and values end up in the pages a focused
- * step reads.  focus_chunk_plan_rows, focus_chunk_qk_norm_rope and focus_chunk_attention are called as a user
- * would call them, with the plan's outputs.
+ * step reads.  focus_chunk_plan_rows, focus_chunk_qk_norm_rope and focus_chunk_attention are called with the plan's
+ * outputs.  In bf16 without head norms the projection's epilogue rotates, from float32 with one rounding as in the step;
+ * with head norms the projection is rounded to bf16 before them.  (So it is without them where max_pages_per_req * S of
+ * `chunk` is beyond the 64 max_pages_per_req + max_block positions of ctx's table of angles.)
  *   - `chunk` was made for the same model geometry (layers, heads, head_dim, dtype, rope_theta) on the same device;
  *   - plan->max_rows <= max_requests * max_block of `ctx` (its workspace holds the rows);
  *   - plan->prefix_len is updated in place to kv_len (declared const for the plan, which only reads it), so a
@@ -468,7 +470,7 @@ int focus_chunk_attention(focus_chunk_ctx* ctx, const focus_chunk_attn* p, void*
  *   - hidden: optional [max_rows, D] float32, the residual stream after the last layer in row order (rows past
  *     the last are undefined).  Without it the last layer stops at its cache write, all that a prefix needs.
  * A token id outside [0, V) sets FOCUS_DEVERR_TOKEN_ID in ctx's error word and is read as 0; new_len beyond max_new
- * sets FOCUS_DEVERR_ROWS there.  Asynchronous, no host sync, can be captured.  Must not overlap another call of
+ * sets FOCUS_DEVERR_ROWS there, and what such a request gets in its pages and in hidden is undefined.  Asynchronous, no host sync, can be captured.  Must not overlap another call of
  * either context.  Returns as focus_step and the chunk calls. */
 typedef struct {
     const focus_chunk_plan* plan;     /* HOST struct of device pointers */
