@@ -42,7 +42,7 @@ struct ChunkAttnDev {
     float scale;
     // bf16: the few-row and the tile kernel both run in this call.  They share nothing, so the tile kernel does not wait for
     // the other one: its CTAs start as the SMs come free, and it only waits at its end, so that who waits for it
-    // has waited for both (40 single tokens and 8 chunks: 308 -> 292 us).
+    // has waited for both (40 single tokens and 8 chunks, short runs: 308 -> 292 us).
     bool pair;
     bool small_walk;  // the launch's key blocks fit 31 bits, as long as the requests' row ranges do not overlap
     // scratch of units whose key walk is split over CTAs: slot 2c / 2c + 1 is CTA c's first / last piece
@@ -53,8 +53,8 @@ struct ChunkAttnDev {
     int* err;
 };
 // bf16 models: requests of at most kChunkFewRows query vectors per KV head (single tokens) go to one kernel, the others
-// to the tile kernel.  16 is what one mma.sync tile holds.  Measured, few / tile kernel, 32/8 heads: 256 single tokens
-// 204 / 290 us, 256 requests of 4 tokens (16 vectors) 237 / 296 us, 32 of them 47 / 56 us.
+// to the tile kernel.  16 is what one mma.sync tile holds.  Measured over seconds, few / tile kernel, 32/8 heads: 256 single
+// tokens 216 / 319 us (1.80 / 1.69 GHz), 256 requests of 4 tokens (16 vectors) 242 / 327, 32 of them 48 / 55.
 constexpr int kChunkFewRows = 16;
 constexpr int kChunkTileRows = 256;  // query vectors per unit of the tile kernel
 int launch_chunk_attention_few(const ChunkAttnDev& a, int sms, cudaStream_t s);

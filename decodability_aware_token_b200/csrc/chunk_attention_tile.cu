@@ -23,11 +23,12 @@
 //
 // Bound by the tensor core and the softmax side by side: a pair of blocks keeps the tensor core for 1360 cycles (S at
 // 52 a K step of 16, its operands read from shared memory as fast as that goes, P V at 66) and the exponential unit
-// for 1062 of the 1800 that it takes.  The 8192-token prompt (16/8 heads) takes 279 us, 985 TFLOP/s at 1.5 to 1.6 GHz,
-// where the card's power management holds it.  When it took 290, leaving out the MMAs left 265, leaving out the
-// softmax's arithmetic 283, and leaving out both, which is the copies out of L2, 205.  Two chunks of 1024 tokens over
-// 65000 cached, 32/8 heads: 2230 us in short runs, 2450 in long ones.
-// Why this shape: with 128 keys a block only one S buffer per tile fits in TMEM, and the prompt took 368 us; with
+// for 1062 of the 1800 that it takes.  Measured over seconds, at the clock where the card's power management
+// holds it: the 8192-token prompt (16/8 heads) 308 us at 1.79 GHz, 892 TFLOP/s (287 in short runs; 316 and 323 on other
+// cards); two chunks of 1024 tokens over 65000 cached, 32/8 heads, 2519 us at 1.43 GHz, 878 TFLOP/s.  In short runs,
+// when the prompt took 290, leaving out the MMAs left 265, leaving out the softmax's arithmetic 283, and leaving out both,
+// which is the copies out of L2, 205.
+// Why this shape (short runs): with 128 keys a block only one S buffer per tile fits in TMEM, and the prompt took 368 us; with
 // one MMA warp for both tiles and one S buffer 347 us; with two threads per query vector (16 softmax warps) 325 against
 // 290; with the two tiles' exponentials kept half a block apart 302.
 //

@@ -105,7 +105,9 @@ __device__ void chunk_schedule(const ChunkAttnDev& a, const ChunkShape& sh, long
                                ChunkRange* out) {
     const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
     // Tiles one thread counts by itself; a request of more takes the general way below, with its 64-bit scans.  (A
-    // prompt of 8192 tokens has 64; its attention as a whole takes 279 us this way, 287 the other.)
+    // prompt of 8192 tokens has 64: its attention took 279 us this way, 287 the other, in short runs.  At the limit both take
+    // as long, over seconds: a prompt of 128 tiles 1090 us this way, 1095 the other; one of 129 tiles 1107 and 1109; one of
+    // 128 beside 200 short chunks 1433 and 1439.)
     constexpr int kSerial = 128;
     int any_long = 0;
     if (a.N <= nt && a.small_walk) {
