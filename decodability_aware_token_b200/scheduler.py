@@ -176,7 +176,10 @@ def share_rows(left: List[int], rows: int, step: int) -> List[int]:
 class EffectiveBatchScheduler:
     """Continuous batching of block-diffusion requests over `slots` batch slots (see the module notes).
 
-    engine:       object with step(view, dense) and commit(view) acting in place on slot views
+    engine:       object with step(view, dense) and commit(view) acting in place on slot views.  For requests with
+                  prompt_tokens also prefill_rows(), the tokens a call takes, and prefill(view, tokens, new_len, pages)
+                  with the arguments on the host; mask_block (default 1) and prefill_requests() (slots a call takes,
+                  default all) where they apply
     kv_pool:      [pages, L, 2, Hkv, S, d] tensor shared by every request (prompts already written)
     free_pages:   pool pages not holding any prompt, available for generated blocks
     mask_token:   token id of a masked position (the block starts all masked)
